@@ -1,0 +1,403 @@
+// kv_api.cuh -- C entry points of the rotary positions and of the quantised
+// cache of recent tokens (milo.h): argument checks and launches.  Included by
+// milo.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+bool float_dtype(milo_dtype t) { return t == MILO_F32 || t == MILO_BF16; }
+
+// ------------------------------------------------------------------ rotary
+
+milo_status rope_check(const milo_rope_params *p, int *rd) {
+    if (!p || p->d < 2 || p->d % 2 || p->rotary_dim < 0 || p->rotary_dim % 2 || p->rotary_dim > p->d)
+        return MILO_ERR_INVALID_ARG;
+    if (p->d > MILO_ROPE_MAX_D) return MILO_ERR_UNSUPPORTED;
+    *rd = p->rotary_dim ? p->rotary_dim : p->d;
+    if (!(p->base > 1.0) || !std::isfinite(p->base) || !std::isfinite(p->attn_factor) || p->attn_factor < 0.0)
+        return MILO_ERR_INVALID_ARG;
+    if (p->scaling < MILO_ROPE_NONE || p->scaling > MILO_ROPE_BANDS) return MILO_ERR_INVALID_ARG;
+    if (p->scaling != MILO_ROPE_NONE && (!(p->factor > 0.0) || !std::isfinite(p->factor)))
+        return MILO_ERR_INVALID_ARG;
+    if (p->scaling == MILO_ROPE_NTK && *rd <= 2) return MILO_ERR_INVALID_ARG;
+    if (p->scaling >= MILO_ROPE_YARN && (!(p->orig_ctx > 0.0) || !std::isfinite(p->orig_ctx)))
+        return MILO_ERR_INVALID_ARG;
+    if (p->scaling == MILO_ROPE_YARN && !(p->beta_slow > 0.0 && p->beta_fast >= p->beta_slow &&
+                                          std::isfinite(p->beta_fast)))
+        return MILO_ERR_INVALID_ARG;
+    if (p->scaling == MILO_ROPE_BANDS && !(p->high_freq > p->low_freq && std::isfinite(p->low_freq) &&
+                                           std::isfinite(p->high_freq)))
+        return MILO_ERR_INVALID_ARG;
+    return MILO_OK;
+}
+
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+
+double clamp01(double x) { return x < 0.0 ? 0.0 : (x > 1.0 ? 1.0 : x); }
+
+// w_i and the factor on the turned channels (milo.h, milo_rope_scaling)
+void rope_freqs(const milo_rope_params *p, int rd, double *w, double *m) {
+    const double base = p->scaling == MILO_ROPE_NTK ? p->base * std::pow(p->factor, (double)rd / (rd - 2)) : p->base;
+    double lo = 0.0, span = 1.0;
+    if (p->scaling == MILO_ROPE_YARN) {
+        auto channel = [&](double turns) { return rd * std::log(p->orig_ctx / (turns * kTwoPi)) / (2.0 * std::log(base)); };
+        lo = std::max(std::floor(channel(p->beta_fast)), 0.0);
+        const double hi = std::min(std::ceil(channel(p->beta_slow)), (double)rd - 1.0);
+        span = hi > lo ? hi - lo : 0.001;
+    }
+    for (int i = 0; i < rd / 2; ++i) {
+        const double t = std::pow(base, -2.0 * i / rd);
+        switch (p->scaling) {
+        case MILO_ROPE_LINEAR: w[i] = t / p->factor; break;
+        case MILO_ROPE_YARN: {
+            const double g = clamp01((i - lo) / span);
+            w[i] = t / p->factor * g + t * (1.0 - g);
+            break;
+        }
+        case MILO_ROPE_BANDS: {
+            const double u = clamp01((p->orig_ctx * t / kTwoPi - p->low_freq) / (p->high_freq - p->low_freq));
+            w[i] = (1.0 - u) * t / p->factor + u * t;
+            break;
+        }
+        default: w[i] = t;
+        }
+    }
+    *m = p->attn_factor > 0.0 ? p->attn_factor
+                              : (p->scaling == MILO_ROPE_YARN ? 0.1 * std::log(p->factor) + 1.0 : 1.0);
+}
+
+// [lo, hi) bytes that n_tokens x n_heads rows of d elements cover
+void rope_extent(const void *p, int64_t ts, int64_t hs, int64_t nt, int64_t nh, int d, int es, uintptr_t &lo,
+                 uintptr_t &hi) {
+    lo = (uintptr_t)p;
+    hi = lo + (uintptr_t)(((nt - 1) * ts + (nh - 1) * hs + d) * es);
+}
+
+// ------------------------------------------------------------------- cache
+
+bool kv_ok(const milo_kv_shape *s) {
+    return s && s->L > 0 && s->S > 0 && s->H > 0 && s->cap > 0 && s->cap <= (1 << 26) && s->block_len >= 16 &&
+           s->block_len <= 1024 && s->block_len % 16 == 0 &&
+           (s->dtype == MILO_INT8 || s->dtype == MILO_FP8 || s->dtype == MILO_INT4) &&
+           (int64_t)s->S * s->H <= INT32_MAX && (int64_t)s->L * s->S * s->H <= INT32_MAX;
+}
+
+milo_status kv_check(const milo_kv_shape *s, const void *cache, size_t bytes) {
+    if (!kv_ok(s) || !cache || !aligned(cache, kAlign)) return MILO_ERR_INVALID_ARG;
+    if (s->d != D) return MILO_ERR_UNSUPPORTED;
+    return bytes < milo_kv_cache_size(s) ? MILO_ERR_WORKSPACE : MILO_OK;
+}
+
+KvView kv_view(const milo_kv_shape *s, const void *cache) {
+    KvView v{};
+    v.base = (unsigned char *)const_cast<void *>(cache);
+    v.L = s->L; v.S = s->S; v.H = s->H; v.cap = s->cap; v.block_len = s->block_len;
+    v.n_b = (s->cap + s->block_len - 1) / s->block_len;
+    v.dtype = s->dtype;
+    const int64_t sh = (int64_t)s->S * s->H, rows = sh * s->cap, blocks = sh * v.n_b;
+    const int64_t size[7] = {rows * v.row_bytes(), rows * v.row_bytes(), rows * v.par_bytes(), rows * v.par_bytes(),
+                             blocks * 2 * D * 2, blocks * 2 * D, blocks * 4};
+    int64_t at = 0;
+    for (int i = 0; i < 7; ++i) {
+        v.off[i] = at;
+        at = (int64_t)align_up((size_t)(at + size[i]));
+    }
+    v.layer = at;
+    return v;
+}
+
+// the candidates, queries and heads of a select or attention call
+milo_status kv_query_check(const milo_kv_shape *s, const void *q, milo_dtype q_dtype, int32_t n_q, int32_t Hq,
+                           const int32_t *len) {
+    if (!q || !len || n_q <= 0 || Hq <= 0 || Hq % s->H || !aligned(q, 16) || !aligned(len, 4))
+        return MILO_ERR_INVALID_ARG;
+    if (!float_dtype(q_dtype)) return MILO_ERR_UNSUPPORTED;
+    if ((int64_t)s->L * s->S * n_q * Hq > INT32_MAX) return MILO_ERR_UNSUPPORTED;
+    return MILO_OK;
+}
+
+// grid size for `ctas` thread blocks in x, 0 if there are too many
+unsigned grid_x(int64_t ctas) { return ctas > INT32_MAX ? 0u : (unsigned)ctas; }
+
+template <typename T> void kv_append_launch(const KvAppendArgs &a, unsigned grid, cudaStream_t s) {
+    const int threads = 32 * KV_APPEND_WARPS;
+    if (a.c.dtype == MILO_INT8) k_kv_append<T, MILO_INT8><<<grid, threads, 0, s>>>(a);
+    else if (a.c.dtype == MILO_FP8) k_kv_append<T, MILO_FP8><<<grid, threads, 0, s>>>(a);
+    else k_kv_append<T, MILO_INT4><<<grid, threads, 0, s>>>(a);
+}
+
+template <typename T> void kv_read_launch(const KvReadArgs &a, dim3 grid, cudaStream_t s) {
+    if (a.c.dtype == MILO_INT8) k_kv_read<T, MILO_INT8><<<grid, 256, 0, s>>>(a);
+    else if (a.c.dtype == MILO_FP8) k_kv_read<T, MILO_FP8><<<grid, 256, 0, s>>>(a);
+    else k_kv_read<T, MILO_INT4><<<grid, 256, 0, s>>>(a);
+}
+
+template <typename T> void kv_attn_rows_launch(const KvAttnArgs &a, int64_t rows, cudaStream_t s) {
+    const unsigned grid = (unsigned)((rows + 3) / 4);
+    if (a.c.dtype == MILO_INT8) k_kv_attn_rows<T, MILO_INT8><<<grid, 128, 0, s>>>(a);
+    else if (a.c.dtype == MILO_FP8) k_kv_attn_rows<T, MILO_FP8><<<grid, 128, 0, s>>>(a);
+    else k_kv_attn_rows<T, MILO_INT4><<<grid, 128, 0, s>>>(a);
+}
+
+milo_status kv_attn_launch(const milo_kv_shape *shape, const void *cache, const void *q, milo_dtype q_dtype,
+                           int32_t n_q, int32_t Hq, const int32_t *len, const int32_t *selected, int32_t n_sel,
+                           double scale, void *out, float *lse, float2 *ml, void *workspace, cudaStream_t s) {
+    (void)workspace;
+    KvAttnArgs a{};
+    a.c = kv_view(shape, cache);
+    a.q = q; a.out = out; a.lse = lse; a.ml = ml; a.len = len; a.sel = selected;
+    a.n_q = n_q; a.G = Hq / shape->H; a.n_sel = n_sel;
+    a.scale = scale > 0.0 ? (float)scale : (float)(1.0 / std::sqrt((double)D));
+    const int64_t rows = (int64_t)shape->L * shape->S * n_q * Hq;
+    if (q_dtype == MILO_BF16) kv_attn_rows_launch<__nv_bfloat16>(a, rows, s);
+    else kv_attn_rows_launch<float>(a, rows, s);
+    return cuda_check(cudaGetLastError(), "kv attention launch");
+}
+
+// selection of a call: NULL and 0, or ids and 1 .. n_b of them
+bool kv_selection_ok(const milo_kv_shape *s, const int32_t *selected, int32_t n_sel) {
+    if (!selected) return n_sel == 0;
+    return aligned(selected, 4) && n_sel >= 1;
+}
+
+}  // namespace
+
+extern "C" {
+
+void milo_rope_default_params(milo_rope_params *p, int32_t d, double base) {
+    if (!p) return;
+    *p = milo_rope_params{d, 0, 0, MILO_ROPE_NONE, base, 1.0, 0.0, 32.0, 1.0, 1.0, 4.0, 0.0};
+}
+
+milo_status milo_rope_freqs(const milo_rope_params *p, double *w, double *attn_factor) {
+    int rd;
+    const milo_status st = rope_check(p, &rd);
+    if (st != MILO_OK) return st;
+    double f[MILO_ROPE_MAX_D / 2], m;
+    rope_freqs(p, rd, f, &m);
+    if (w) memcpy(w, f, sizeof(double) * (rd / 2));
+    if (attn_factor) *attn_factor = m;
+    return MILO_OK;
+}
+
+milo_status milo_rope(const milo_rope_params *p, const void *x, milo_dtype x_dtype, int64_t xt, int64_t xh, void *y,
+                      milo_dtype y_dtype, int64_t yt, int64_t yh, const int32_t *positions, int64_t n_pos,
+                      int64_t n_tokens, int32_t n_heads, int32_t transpose, milo_stream_t stream) {
+    int rd;
+    milo_status st = rope_check(p, &rd);
+    if (st != MILO_OK) return st;
+    if (!float_dtype(x_dtype) || !float_dtype(y_dtype)) return MILO_ERR_UNSUPPORTED;
+    if (n_tokens < 0 || n_heads < 0) return MILO_ERR_INVALID_ARG;
+    if (n_tokens == 0 || n_heads == 0) return MILO_OK;
+    const int ex = x_dtype == MILO_F32 ? 4 : 2, ey = y_dtype == MILO_F32 ? 4 : 2, d = p->d;
+    if (!x || !y || !positions || n_pos < 1 || xt < 0 || xh < 0 || yt < 0 || yh < 0 || !aligned(x, ex) ||
+        !aligned(y, ey) || !aligned(positions, 4))
+        return MILO_ERR_INVALID_ARG;
+    const int64_t most = int64_t(1) << 46;   // strides and counts whose products stay inside 64 bits
+    if (xt > most / n_tokens || xh > most / n_heads || yt > most / n_tokens || yh > most / n_heads || n_tokens > most)
+        return MILO_ERR_INVALID_ARG;
+    // rows of y apart: one index strides over whole rows of the other
+    const bool apart = (n_heads == 1 || yh >= d) && (n_tokens == 1 || yt >= (n_heads - 1) * yh + d);
+    const bool apart2 = (n_tokens == 1 || yt >= d) && (n_heads == 1 || yh >= (n_tokens - 1) * yt + d);
+    if (!apart && !apart2) return MILO_ERR_INVALID_ARG;
+    const bool same = x == y && x_dtype == y_dtype && (xt == yt || n_tokens == 1) && (xh == yh || n_heads == 1);
+    if (!same) {
+        uintptr_t x0, x1, y0, y1;
+        rope_extent(x, xt, xh, n_tokens, n_heads, d, ex, x0, x1);
+        rope_extent(y, yt, yh, n_tokens, n_heads, d, ey, y0, y1);
+        if (x0 < y1 && y0 < x1) return MILO_ERR_INVALID_ARG;
+    }
+    RopeArgs a{};
+    double w[MILO_ROPE_MAX_D / 2], m;
+    rope_freqs(p, rd, w, &m);
+    for (int i = 0; i < rd / 2; ++i) a.turns[i] = w[i] / kTwoPi;
+    a.x = x; a.y = y; a.pos = positions; a.n_pos = n_pos; a.n_tokens = n_tokens;
+    a.xt = xt; a.xh = xh; a.yt = yt; a.yh = yh; a.d = d; a.rd = rd; a.heads = n_heads;
+    a.m = (float)m;
+    a.sgn = transpose ? -1.f : 1.f;
+    // widest access that every row start and both parts of a row allow
+    const bool inter = p->interleaved != 0;
+    int v = 8;
+    auto fits = [&](int n) {
+        const int64_t unit = inter ? rd : rd / 2;
+        return unit % n == 0 && d % n == 0 && xt % n == 0 && xh % n == 0 && yt % n == 0 && yh % n == 0 &&
+               aligned(x, (size_t)std::min(16, n * ex)) && aligned(y, (size_t)std::min(16, n * ey));
+    };
+    if (!fits(8)) v = fits(4) ? 4 : (inter ? 2 : 1);
+    a.rot_units = (inter ? rd : rd / 2) / v;
+    a.units = a.rot_units + (same ? 0 : (d - rd) / v);   // in place, the other channels are where they belong
+    // a thread takes as many heads as leave a full wave of threads
+    const int64_t per_head = n_tokens * a.units, wave = (int64_t)sm_count() * 2048;
+    a.hpt = (int)std::min<int64_t>(n_heads, std::max<int64_t>(1, per_head * n_heads / wave));
+    a.n_hc = (n_heads + a.hpt - 1) / a.hpt;
+    if (grid_x((per_head * a.n_hc + 255) / 256) == 0) return MILO_ERR_UNSUPPORTED;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaEvent_t t0 = tmark(s);
+    auto go = [&](auto tx, auto ty) {
+        using TX = decltype(tx);
+        using TY = decltype(ty);
+        if (v == 8) rope_launch_layout<TX, TY, 8>(a, inter, s);
+        else if (v == 4) rope_launch_layout<TX, TY, 4>(a, inter, s);
+        else rope_launch_layout<TX, TY, 1>(a, inter, s);
+    };
+    if (x_dtype == MILO_F32) y_dtype == MILO_F32 ? go(0.f, 0.f) : go(0.f, __nv_bfloat16());
+    else y_dtype == MILO_F32 ? go(__nv_bfloat16(), 0.f) : go(__nv_bfloat16(), __nv_bfloat16());
+    tpush(MILO_TK_ROPE, t0, tmark(s));
+    return cuda_check(cudaGetLastError(), "rope launch");
+}
+
+size_t milo_kv_cache_size(const milo_kv_shape *shape) {
+    if (!kv_ok(shape) || shape->d != D) return 0;
+    return (size_t)kv_view(shape, nullptr).layer * shape->L;
+}
+
+milo_status milo_kv_layout(const milo_kv_shape *shape, size_t *offsets) {
+    if (!kv_ok(shape) || !offsets) return MILO_ERR_INVALID_ARG;
+    if (shape->d != D) return MILO_ERR_UNSUPPORTED;
+    const KvView v = kv_view(shape, nullptr);
+    for (int i = 0; i < 7; ++i) offsets[i] = (size_t)v.off[i];
+    return MILO_OK;
+}
+
+milo_status milo_kv_append(const milo_kv_shape *shape, void *cache, size_t cache_bytes, const void *k, const void *v,
+                           milo_dtype in_dtype, const int64_t *strides, int32_t n_new, const int32_t *start,
+                           const int32_t *count, milo_stream_t stream) {
+    milo_status st = kv_check(shape, cache, cache_bytes);
+    if (st != MILO_OK) return st;
+    if (!float_dtype(in_dtype)) return MILO_ERR_UNSUPPORTED;
+    if (n_new < 0 || n_new > shape->cap) return MILO_ERR_INVALID_ARG;
+    if (n_new == 0) return MILO_OK;
+    if (!k || !v || !start || !aligned(k, 16) || !aligned(v, 16) || !aligned(start, 4) || !aligned(count, 4))
+        return MILO_ERR_INVALID_ARG;
+    KvAppendArgs a{};
+    a.c = kv_view(shape, cache);
+    a.k = k; a.v = v; a.n_new = n_new; a.start = start; a.count = count;
+    a.st = D;
+    a.sh = (int64_t)n_new * D;
+    a.ss = a.sh * shape->H;
+    a.sl = a.ss * shape->S;
+    if (strides) {
+        for (int i = 0; i < 4; ++i)
+            if (strides[i] < 0 || strides[i] % 8) return MILO_ERR_INVALID_ARG;
+        a.sl = strides[0]; a.ss = strides[1]; a.sh = strides[2]; a.st = strides[3];
+    }
+    a.windows = (int)(((int64_t)n_new - 2 + shape->block_len) / shape->block_len) + 1;
+    const unsigned grid = grid_x((int64_t)a.windows * shape->L * shape->S * shape->H * 2);
+    if (!grid) return MILO_ERR_UNSUPPORTED;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaEvent_t t0 = tmark(s);
+    if (in_dtype == MILO_BF16) kv_append_launch<__nv_bfloat16>(a, grid, s);
+    else kv_append_launch<float>(a, grid, s);
+    tpush(MILO_TK_KV_WRITE, t0, tmark(s));
+    return cuda_check(cudaGetLastError(), "kv append launch");
+}
+
+milo_status milo_kv_read(const milo_kv_shape *shape, const void *cache, size_t cache_bytes, int32_t n,
+                         const int32_t *start, const int32_t *count, void *k_out, void *v_out, milo_dtype out_dtype,
+                         milo_stream_t stream) {
+    milo_status st = kv_check(shape, cache, cache_bytes);
+    if (st != MILO_OK) return st;
+    if (!float_dtype(out_dtype)) return MILO_ERR_UNSUPPORTED;
+    if (n < 0 || n > shape->cap) return MILO_ERR_INVALID_ARG;
+    if (n == 0) return MILO_OK;
+    if ((!k_out && !v_out) || !start || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(start, 4) ||
+        !aligned(count, 4))
+        return MILO_ERR_INVALID_ARG;
+    KvReadArgs a{};
+    a.c = kv_view(shape, cache);
+    a.k = k_out; a.v = v_out; a.n = n; a.start = start; a.count = count;
+    a.rows = (int64_t)shape->L * shape->S * shape->H * n;
+    const unsigned grid = grid_x((a.rows * 8 + 255) / 256);
+    if (!grid) return MILO_ERR_UNSUPPORTED;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaEvent_t t0 = tmark(s);
+    if (out_dtype == MILO_BF16) kv_read_launch<__nv_bfloat16>(a, dim3(grid, 2), s);
+    else kv_read_launch<float>(a, dim3(grid, 2), s);
+    tpush(MILO_TK_KV_READ, t0, tmark(s));
+    return cuda_check(cudaGetLastError(), "kv read launch");
+}
+
+size_t milo_kv_select_workspace_size(const milo_kv_shape *shape, int32_t n_q) {
+    if (!kv_ok(shape) || shape->d != D || n_q <= 0) return 0;
+    const int64_t n_b = (shape->cap + shape->block_len - 1) / shape->block_len;
+    return align_up(sizeof(float) * (size_t)((int64_t)shape->L * shape->S * shape->H * n_q * n_b));
+}
+
+milo_status milo_kv_select(const milo_kv_shape *shape, const void *cache, size_t cache_bytes, const void *q,
+                           milo_dtype q_dtype, int32_t n_q, int32_t Hq, const int32_t *len, int32_t n_sel,
+                           int32_t n_first, int32_t n_last, int32_t *selected, float *scores, void *workspace,
+                           size_t ws_bytes, milo_stream_t stream) {
+    milo_status st = kv_check(shape, cache, cache_bytes);
+    if (st != MILO_OK) return st;
+    st = kv_query_check(shape, q, q_dtype, n_q, Hq, len);
+    if (st != MILO_OK) return st;
+    KvSelectArgs a{};
+    a.c = kv_view(shape, cache);
+    if (!selected || !workspace || !aligned(selected, 4) || !aligned(scores, 4) || !aligned(workspace, kAlign) ||
+        n_sel < 1 || n_sel > a.c.n_b || n_first < 0 || n_last < 0 || (int64_t)n_first + n_last > n_sel)
+        return MILO_ERR_INVALID_ARG;
+    if (ws_bytes < milo_kv_select_workspace_size(shape, n_q)) return MILO_ERR_WORKSPACE;
+    a.q = q; a.len = len; a.selected = selected; a.scores = scores ? scores : (float *)workspace;
+    a.n_q = n_q; a.G = Hq / shape->H; a.n_sel = n_sel; a.n_first = n_first; a.n_last = n_last;
+    const unsigned rows = grid_x((int64_t)shape->L * shape->S * n_q * shape->H);
+    const dim3 grid(rows, (unsigned)((a.c.n_b + KV_SCORE_THREADS - 1) / KV_SCORE_THREADS));
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaEvent_t t0 = tmark(s);
+    if (q_dtype == MILO_BF16) k_kv_score<__nv_bfloat16><<<grid, KV_SCORE_THREADS, 0, s>>>(a);
+    else k_kv_score<float><<<grid, KV_SCORE_THREADS, 0, s>>>(a);
+    k_kv_topn<<<rows, KV_TOPN_THREADS, 0, s>>>(a);
+    tpush(MILO_TK_KV_SELECT, t0, tmark(s));
+    return cuda_check(cudaGetLastError(), "kv select launch");
+}
+
+size_t milo_kv_attn_workspace_size(const milo_kv_shape *shape, int32_t n_q, int32_t Hq, int32_t n_sel) {
+    if (!kv_ok(shape) || shape->d != D || n_q <= 0 || Hq <= 0 || Hq % shape->H || n_sel < 0) return 0;
+    return kAlign;
+}
+
+milo_status milo_kv_attn(const milo_kv_shape *shape, const void *cache, size_t cache_bytes, const void *q,
+                         milo_dtype q_dtype, int32_t n_q, int32_t Hq, const int32_t *len, const int32_t *selected,
+                         int32_t n_sel, double scale, void *out, float *lse, void *workspace, size_t ws_bytes,
+                         milo_stream_t stream) {
+    milo_status st = kv_check(shape, cache, cache_bytes);
+    if (st != MILO_OK) return st;
+    st = kv_query_check(shape, q, q_dtype, n_q, Hq, len);
+    if (st != MILO_OK) return st;
+    if (!out || !workspace || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, kAlign) ||
+        !kv_selection_ok(shape, selected, n_sel) || !(scale >= 0.0) || !std::isfinite(scale))
+        return MILO_ERR_INVALID_ARG;
+    if (ws_bytes < milo_kv_attn_workspace_size(shape, n_q, Hq, n_sel)) return MILO_ERR_WORKSPACE;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaEvent_t t0 = tmark(s);
+    st = kv_attn_launch(shape, cache, q, q_dtype, n_q, Hq, len, selected, n_sel, scale, out, lse, nullptr, workspace, s);
+    tpush(MILO_TK_KV_ATTN, t0, tmark(s));
+    return st;
+}
+
+size_t milo_decode_kv_workspace_size(const milo_factors *f, int32_t S, int32_t Hq, int32_t n_sel,
+                                     const milo_kv_shape *shape, int32_t kv_n_sel) {
+    const size_t base = milo_decode_tail_workspace_size(f, S, Hq, n_sel);
+    const size_t kv = milo_kv_attn_workspace_size(shape, 1, Hq, kv_n_sel);
+    return base && kv ? base + kv : 0;
+}
+
+milo_status milo_decode_attn_kv(const milo_factors *f, const float *q, int32_t S, int32_t Hq, const int32_t *selected,
+                                const int32_t *positions, int32_t n_sel, double rope_base, const milo_kv_shape *shape,
+                                const void *cache, size_t cache_bytes, const int32_t *len, const int32_t *kv_selected,
+                                int32_t kv_n_sel, float *out, void *workspace, size_t ws_bytes, milo_stream_t stream) {
+    milo_status st = kv_check(shape, cache, cache_bytes);
+    if (st != MILO_OK) return st;
+    if (!f || shape->L != f->shape.L || shape->H != f->shape.H || shape->S != S) return MILO_ERR_INVALID_ARG;
+    st = kv_query_check(shape, q, MILO_F32, 1, Hq, len);
+    if (st != MILO_OK) return st;
+    if (!kv_selection_ok(shape, kv_selected, kv_n_sel)) return MILO_ERR_INVALID_ARG;
+    TailIn t;
+    t.len = len;
+    t.kv = shape;
+    t.kv_cache = cache;
+    t.kv_selected = kv_selected;
+    t.kv_n_sel = kv_n_sel;
+    return decode_impl(f, q, S, Hq, selected, positions, n_sel, rope_base, t, out, workspace, ws_bytes, stream);
+}
+
+}  // extern "C"

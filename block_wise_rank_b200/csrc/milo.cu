@@ -29,6 +29,8 @@
 #include "decode_tail.cuh"
 #include "decode_offload.cuh"
 #include "bm25.cuh"
+#include "rope.cuh"
+#include "kv_attn.cuh"
 
 using namespace milo;
 
@@ -643,13 +645,23 @@ size_t milo_decode_workspace_size(const milo_factors *f, int32_t S, int32_t Hq, 
 }  // extern "C"
 
 namespace {
-// the recent uncompressed tokens of a decode call (k == nullptr: none)
+// the recent uncompressed tokens of a decode call (k == nullptr and kv ==
+// nullptr: none), plain rows or a quantised cache
 struct TailIn {
     const void *k = nullptr, *v = nullptr;
     milo_dtype dtype = MILO_F32;
     int32_t cap = 0;
     const int32_t *len = nullptr;
+    const milo_kv_shape *kv = nullptr;       // quantised: the cache's shape, buffer and selection
+    const void *kv_cache = nullptr;
+    const int32_t *kv_selected = nullptr;
+    int32_t kv_n_sel = 0;
+    bool any() const { return k || kv; }
 };
+
+milo_status kv_attn_launch(const milo_kv_shape *shape, const void *cache, const void *q, milo_dtype q_dtype,
+                           int32_t n_q, int32_t Hq, const int32_t *len, const int32_t *selected, int32_t n_sel,
+                           double scale, void *out, float *lse, float2 *ml, void *workspace, cudaStream_t s);
 
 size_t tail_workspace_bytes(const milo_factors *f, int32_t S, int32_t Hq) {
     const int64_t rows = (int64_t)f->shape.L * S * Hq;
@@ -667,7 +679,9 @@ milo_status decode_impl(const milo_factors *f, const float *q, int32_t S, int32_
     // 2-bit factors decode on the tensor cores only (blocks of at most 512 tokens)
     if (f->params.factor_dtype == MILO_INT2 && f->shape.block_len > 512) return MILO_ERR_UNSUPPORTED;
     const size_t ws_dec = milo_decode_workspace_size(f, S, Hq, n_sel);
-    if (ws_bytes < ws_dec + (tail.k ? tail_workspace_bytes(f, S, Hq) : 0)) return MILO_ERR_WORKSPACE;
+    const size_t ws_tail = tail.any() ? tail_workspace_bytes(f, S, Hq) : 0;
+    const size_t ws_kv = tail.kv ? milo_kv_attn_workspace_size(tail.kv, 1, Hq, tail.kv_n_sel) : 0;
+    if (ws_bytes < ws_dec + ws_tail + ws_kv) return MILO_ERR_WORKSPACE;
     milo_status st = set_smem_attrs();
     if (st != MILO_OK) return st;
     cudaStream_t s = (cudaStream_t)stream;
@@ -760,12 +774,16 @@ milo_status decode_impl(const milo_factors *f, const float *q, int32_t S, int32_
         k_decode_simt<<<dim3(n_b, f->shape.H, f->shape.L), 256, sizeof(DecodeSimtSmem), s>>>(a);
         tpush(MILO_TK_DECODE, t0, tmark(s));
     }
-    if (tail.k) {   // the recent tokens' partial, then merged with the blocks'
+    if (tail.any()) {   // the recent tokens' partial, then merged with the blocks'
         float *tail_o = (float *)(w + ws_dec);
         float2 *tail_ml = (float2 *)(w + ws_dec + align_up(sizeof(float) * rows * D));
         t0 = tmark(s);
         const dim3 grid((unsigned)f->shape.H, (unsigned)S, (unsigned)f->shape.L);
-        if (tail.dtype == MILO_BF16)
+        if (tail.kv) {
+            st = kv_attn_launch(tail.kv, tail.kv_cache, q, MILO_F32, 1, Hq, tail.len, tail.kv_selected, tail.kv_n_sel,
+                                0.0, tail_o, nullptr, tail_ml, w + ws_dec + ws_tail, s);
+            if (st != MILO_OK) return st;
+        } else if (tail.dtype == MILO_BF16)
             k_tail_attn<__nv_bfloat16><<<grid, D, 0, s>>>(a, (const __nv_bfloat16 *)tail.k,
                                                           (const __nv_bfloat16 *)tail.v, tail.cap, tail.len,
                                                           tail_o, tail_ml);
@@ -1188,3 +1206,5 @@ milo_status milo_timeline_read(void *records, uint32_t *counts) {
 #endif
 
 }  // extern "C"
+
+#include "kv_api.cuh"

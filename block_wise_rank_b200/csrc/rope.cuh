@@ -1,0 +1,146 @@
+// rope.cuh -- rotary positions for queries and keys, and their gradient.
+//
+// Pair i of a row turns by the angle p * w_i (Su et al., "RoFormer", 2021):
+// (a, b) -> m (a cos - b sin, a sin + b cos); the transposed map negates the
+// angle and is the gradient.  The turns p * w_i / (2 pi) are taken modulo 1 in
+// fp64, so a position of 2^31 still leaves 22 bits of the angle, and the rest
+// goes through sincospi in fp32 (its argument, at most 1, is rounded to 2^-25).
+//
+// Bound by memory: each row is read and written once.  A thread owns one unit
+// of V pairs (or V copied channels) of one token and walks a chunk of the
+// heads, so a token's angles are computed once per chunk and stay in
+// registers.
+#pragma once
+#include "project_simt.cuh"   // from_f32
+
+namespace milo {
+
+struct RopeArgs {
+    double turns[MILO_ROPE_MAX_D / 2];   // w_i / (2 pi)
+    const void *x;
+    void *y;
+    const int32_t *pos;
+    int64_t n_pos, n_tokens;
+    int64_t xt, xh, yt, yh;              // strides in elements
+    int d, rd, heads;
+    int hpt, n_hc;                       // heads per thread, chunks of heads
+    int units, rot_units;                // units of a row, those that turn
+    float m;                             // factor on the turned channels
+    float sgn;                           // -1: transposed
+};
+
+template <typename T, int V> __device__ __forceinline__ void rope_load(const T *p, float (&v)[V]) {
+    constexpr int B = V * (int)sizeof(T);
+    if constexpr (B % 16 == 0) {
+        uint4 w[B / 16];
+#pragma unroll
+        for (int i = 0; i < B / 16; ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
+        const T *e = reinterpret_cast<const T *>(w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = to_f32(e[i]);
+    } else if constexpr (B == 8 && V >= 4) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(p);
+        const T *e = reinterpret_cast<const T *>(&w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = to_f32(e[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = to_f32(p[i]);
+    }
+}
+
+template <typename T, int V> __device__ __forceinline__ void rope_store(T *p, const float (&v)[V]) {
+    constexpr int B = V * (int)sizeof(T);
+    if constexpr (B % 16 == 0) {
+        uint4 w[B / 16];
+        T *e = reinterpret_cast<T *>(w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) e[i] = from_f32<T>(v[i]);
+#pragma unroll
+        for (int i = 0; i < B / 16; ++i) reinterpret_cast<uint4 *>(p)[i] = w[i];
+    } else if constexpr (B == 8 && V >= 4) {
+        uint2 w;
+        T *e = reinterpret_cast<T *>(&w);
+#pragma unroll
+        for (int i = 0; i < V; ++i) e[i] = from_f32<T>(v[i]);
+        *reinterpret_cast<uint2 *>(p) = w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i] = from_f32<T>(v[i]);
+    }
+}
+
+// V elements per access.  INTER: a unit is V neighbouring channels (V / 2
+// pairs); otherwise V pairs (i, i + rd / 2), i.e. two accesses.
+template <typename TX, typename TY, int V, bool INTER>
+__global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeArgs a) {
+    const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const int u = (int)(gid % a.units);
+    const int64_t r = gid / a.units;
+    const int hc = (int)(r % a.n_hc);
+    const int64_t t = r / a.n_hc;
+    if (t >= a.n_tokens) return;
+    const int h0 = hc * a.hpt, h1 = min(a.heads, h0 + a.hpt);
+    const TX *x = (const TX *)a.x + t * a.xt;
+    TY *y = (TY *)a.y + t * a.yt;
+    if (u >= a.rot_units) {   // channels that do not turn
+        const int c = a.rd + (u - a.rot_units) * V;
+        for (int h = h0; h < h1; ++h) {
+            float v[V];
+            rope_load<TX, V>(x + h * a.xh + c, v);
+            rope_store<TY, V>(y + h * a.yh + c, v);
+        }
+        return;
+    }
+    constexpr int NP = INTER ? (V + 1) / 2 : V;   // pairs of a unit
+    const double p = (double)a.pos[t % a.n_pos];
+    float cs[NP], sn[NP];
+    const int i0 = u * NP;
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const double n = p * a.turns[i0 + i];
+        float s, c;
+        sincospif((float)(2.0 * (n - rint(n))), &s, &c);
+        cs[i] = c * a.m;
+        sn[i] = s * a.m * a.sgn;
+    }
+    if constexpr (INTER) {
+        static_assert(V % 2 == 0, "a unit of neighbouring channels holds whole pairs");
+        for (int h = h0; h < h1; ++h) {
+            float v[V], w[V];
+            rope_load<TX, V>(x + h * a.xh + u * V, v);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                w[2 * i] = v[2 * i] * cs[i] - v[2 * i + 1] * sn[i];
+                w[2 * i + 1] = v[2 * i] * sn[i] + v[2 * i + 1] * cs[i];
+            }
+            rope_store<TY, V>(y + h * a.yh + u * V, w);
+        }
+    } else {
+        const int c0 = u * V, c1 = a.rd / 2 + u * V;
+        for (int h = h0; h < h1; ++h) {
+            float v[V], w[V], p0[V], p1[V];
+            rope_load<TX, V>(x + h * a.xh + c0, v);
+            rope_load<TX, V>(x + h * a.xh + c1, w);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                p0[i] = v[i] * cs[i] - w[i] * sn[i];
+                p1[i] = v[i] * sn[i] + w[i] * cs[i];
+            }
+            rope_store<TY, V>(y + h * a.yh + c0, p0);
+            rope_store<TY, V>(y + h * a.yh + c1, p1);
+        }
+    }
+}
+
+template <typename TX, typename TY, int V, bool INTER> void rope_launch(const RopeArgs &a, cudaStream_t s) {
+    const int64_t threads = a.n_tokens * a.n_hc * a.units;
+    k_rope<TX, TY, V, INTER><<<(unsigned)((threads + 255) / 256), 256, 0, s>>>(a);
+}
+
+template <typename TX, typename TY, int V> void rope_launch_layout(const RopeArgs &a, bool inter, cudaStream_t s) {
+    if (inter) rope_launch<TX, TY, (V < 2 ? 2 : V), true>(a, s);
+    else rope_launch<TX, TY, V, false>(a, s);
+}
+
+}  // namespace milo

@@ -26,8 +26,10 @@ MILO_ERR_NONFINITE = -5
 MILO_ERR_BOUNDS = -6
 MILO_ERR_TIMEOUT = -7
 
-MILO_F32, MILO_BF16, MILO_INT8, MILO_INT2 = 0, 1, 2, 3
+MILO_F32, MILO_BF16, MILO_INT8, MILO_INT2, MILO_INT4, MILO_FP8 = 0, 1, 2, 3, 4, 5
 DTYPES = {"f32": MILO_F32, "bf16": MILO_BF16, "int8": MILO_INT8, "int2": MILO_INT2}
+KV_DTYPES = {"int8": MILO_INT8, "fp8": MILO_FP8, "int4": MILO_INT4}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
 
 class milo_cache_shape(ctypes.Structure):
@@ -40,6 +42,18 @@ class milo_compress_params(ctypes.Structure):
     _fields_ = [("budget_frac", ctypes.c_double), ("budget_abs", ctypes.c_int64), ("eps_rel", ctypes.c_double),
                 ("eps_scope", ctypes.c_int32), ("r_min", ctypes.c_int32), ("r_max", ctypes.c_int32),
                 ("factor_dtype", ctypes.c_int), ("max_sweeps", ctypes.c_int32), ("jacobi_tol", ctypes.c_float)]
+
+
+class milo_rope_params(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("orig_ctx", ctypes.c_double), ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("low_freq", ctypes.c_double), ("high_freq", ctypes.c_double), ("attn_factor", ctypes.c_double)]
+
+
+class milo_kv_shape(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int32), ("S", ctypes.c_int32), ("H", ctypes.c_int32), ("cap", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("block_len", ctypes.c_int32), ("dtype", ctypes.c_int)]
 
 
 class MiloError(RuntimeError):
@@ -58,13 +72,17 @@ EXPORTS = [
     "milo_jacobi_rounds", "milo_decode_tail_workspace_size", "milo_decode_attn_tail",
     "milo_decode_offload_workspace_size", "milo_decode_attn_offload", "milo_bm25_workspace_size",
     "milo_bm25_select", "milo_factors_shape", "milo_decode_attn_offload_tail",
+    "milo_rope_default_params", "milo_rope_freqs", "milo_rope", "milo_kv_cache_size", "milo_kv_layout",
+    "milo_kv_append", "milo_kv_read", "milo_kv_select_workspace_size", "milo_kv_select",
+    "milo_kv_attn_workspace_size", "milo_kv_attn", "milo_decode_kv_workspace_size", "milo_decode_attn_kv",
 ]
 
 # stages of milo_timing_read, in order (milo_timed_stage)
 TIMED_STAGES = ["gram", "jacobi", "refine", "select", "project", "decode_prep", "decode", "combine", "tail",
-                "stage", "retrieve"]
+                "stage", "retrieve", "rope", "kv_write", "kv_read", "kv_select", "kv_attn"]
 
 MILO_NOALLOC_MAX_BLOCKS = 65536
+MILO_ROPE_MAX_D = 512
 
 
 def lib():
@@ -126,6 +144,27 @@ def lib():
         L.milo_timing_enable.argtypes = [I32]; L.milo_timing_enable.restype = ctypes.c_int
         L.milo_timing_read.argtypes = [P, P, I32]; L.milo_timing_read.restype = ctypes.c_int
         L.milo_jacobi_rounds.argtypes = [P, P, P]; L.milo_jacobi_rounds.restype = ctypes.c_int
+        RP, KP, F64 = ctypes.POINTER(milo_rope_params), ctypes.POINTER(milo_kv_shape), ctypes.c_double
+        L.milo_rope_default_params.argtypes = [RP, I32, F64]; L.milo_rope_default_params.restype = None
+        L.milo_rope_freqs.argtypes = [RP, P, P]; L.milo_rope_freqs.restype = ctypes.c_int
+        L.milo_rope.argtypes = [RP, P, I32, I64, I64, P, I32, I64, I64, P, I64, I64, I32, I32, P]
+        L.milo_rope.restype = ctypes.c_int
+        L.milo_kv_cache_size.argtypes = [KP]; L.milo_kv_cache_size.restype = SZ
+        L.milo_kv_layout.argtypes = [KP, P]; L.milo_kv_layout.restype = ctypes.c_int
+        L.milo_kv_append.argtypes = [KP, P, SZ, P, P, I32, P, I32, P, P, P]
+        L.milo_kv_append.restype = ctypes.c_int
+        L.milo_kv_read.argtypes = [KP, P, SZ, I32, P, P, P, P, I32, P]
+        L.milo_kv_read.restype = ctypes.c_int
+        L.milo_kv_select_workspace_size.argtypes = [KP, I32]; L.milo_kv_select_workspace_size.restype = SZ
+        L.milo_kv_select.argtypes = [KP, P, SZ, P, I32, I32, I32, P, I32, I32, I32, P, P, P, SZ, P]
+        L.milo_kv_select.restype = ctypes.c_int
+        L.milo_kv_attn_workspace_size.argtypes = [KP, I32, I32, I32]; L.milo_kv_attn_workspace_size.restype = SZ
+        L.milo_kv_attn.argtypes = [KP, P, SZ, P, I32, I32, I32, P, P, I32, F64, P, P, P, SZ, P]
+        L.milo_kv_attn.restype = ctypes.c_int
+        L.milo_decode_kv_workspace_size.argtypes = [P, I32, I32, I32, KP, I32]
+        L.milo_decode_kv_workspace_size.restype = SZ
+        L.milo_decode_attn_kv.argtypes = [P, P, I32, I32, P, P, I32, F64, KP, P, SZ, P, P, I32, P, P, SZ, P]
+        L.milo_decode_attn_kv.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -427,6 +466,278 @@ def milo_decode_attn_offload_tail(f: Factors, q: torch.Tensor, selected: torch.T
                                             _ptr(tail_len), _ptr(out), _ptr(workspace), workspace.numel(),
                                             _stream(stream))
     _check(s, "milo_decode_attn_offload_tail")
+    return out
+
+
+# ------------------------------------------------- rotary positions
+def rope_params(d: int, base: float = 1e6, rotary_dim: int = 0, interleaved: bool = False, scaling: str = "none",
+                **kw) -> milo_rope_params:
+    """The C parameters of milo_rope; further fields of milo_rope_params by name."""
+    p = milo_rope_params()
+    lib().milo_rope_default_params(ctypes.byref(p), d, base)
+    p.rotary_dim, p.interleaved, p.scaling = rotary_dim, int(interleaved), ROPE_SCALINGS[scaling]
+    for k, v in kw.items():
+        setattr(p, k, v)
+    return p
+
+
+def milo_rope_freqs(params: milo_rope_params):
+    """(angles per position of every pair as a list, factor on the turned channels)."""
+    w = (ctypes.c_double * (MILO_ROPE_MAX_D // 2))()
+    m = ctypes.c_double()
+    _check(lib().milo_rope_freqs(ctypes.byref(params), ctypes.cast(w, ctypes.c_void_p),
+                                 ctypes.cast(ctypes.byref(m), ctypes.c_void_p)), "milo_rope_freqs")
+    return list(w)[:(params.rotary_dim or params.d) // 2], m.value
+
+
+def _on(t: torch.Tensor, stream):
+    """The stream of a call on t, which lives on the current CUDA device."""
+    if not t.is_cuda:
+        raise ValueError(f"tensor on {t.device}, a CUDA tensor expected")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensor on {t.device}, and the current device is cuda:{torch.cuda.current_device()}")
+    return ctypes.c_void_p((stream or torch.cuda.current_stream()).cuda_stream)
+
+
+def _used_on(stream, *tensors):
+    """Tells the allocator that tensors made here are used on `stream`."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _same_device(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}")
+
+
+def _int32(t: torch.Tensor, shape, what: str):
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what}: contiguous int32 {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+
+
+def milo_rope(x: torch.Tensor, positions: torch.Tensor, params: milo_rope_params, out=None, out_dtype=None,
+              transpose: bool = False, stream=None) -> torch.Tensor:
+    """Rows x [n_tokens][n_heads][d] (fp32 or bf16, any strides, d contiguous)
+    turned to positions int32 [n_pos] (token t takes positions[t % n_pos]);
+    transpose=True gives the gradient with respect to x of a gradient x.
+    out=x turns in place."""
+    if x.dim() != 3 or x.shape[2] != params.d or (x.numel() and x.stride(2) != 1):
+        raise ValueError(f"x: [n_tokens][n_heads][{params.d}] with contiguous rows expected, got {tuple(x.shape)}")
+    s = _on(x, stream)
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    elif out.shape != x.shape or (out.numel() and out.stride(2) != 1):
+        raise ValueError(f"out: {tuple(x.shape)} with contiguous rows expected, got {tuple(out.shape)}")
+    _int32(positions, (positions.numel(),), "positions")
+    _same_device(x.device, out, positions)
+    rc = lib().milo_rope(params, x.data_ptr(), _dtype_code(x.dtype), x.stride(0), x.stride(1), out.data_ptr(),
+                         _dtype_code(out.dtype), out.stride(0), out.stride(1), positions.data_ptr(),
+                         positions.numel(), x.shape[0], x.shape[1], int(transpose), s)
+    _used_on(stream, out)
+    _check(rc, "milo_rope")
+    return out
+
+
+# ------------------------------------- quantised cache of recent tokens
+def kv_shape(L: int, S: int, H: int, cap: int, block_len: int = 64, dtype="int8", d: int = 128) -> milo_kv_shape:
+    return milo_kv_shape(L, S, H, cap, d, block_len, KV_DTYPES[dtype] if isinstance(dtype, str) else dtype)
+
+
+def milo_kv_cache_size(shape: milo_kv_shape) -> int:
+    return lib().milo_kv_cache_size(ctypes.byref(shape))
+
+
+def milo_kv_layout(shape: milo_kv_shape):
+    """Byte offsets of a layer's sections (k, v, k params, v params, bounds, bound codes, bound scales)."""
+    o = (ctypes.c_size_t * 7)()
+    _check(lib().milo_kv_layout(ctypes.byref(shape), ctypes.cast(o, ctypes.c_void_p)), "milo_kv_layout")
+    return list(o)
+
+
+class KvCache:
+    """A quantised cache of recent tokens: its shape and its buffer (uint8,
+    at least milo_kv_cache_size bytes; made on `device` when not given)."""
+
+    def __init__(self, shape: milo_kv_shape, buf=None, device="cuda"):
+        n = milo_kv_cache_size(shape)
+        if n == 0:
+            raise MiloError(MILO_ERR_INVALID_ARG, "milo_kv_cache_size")
+        self.shape = shape
+        self.buf = _bytes(n, device) if buf is None else buf
+        if self.buf.dtype != torch.uint8 or not self.buf.is_contiguous():
+            raise ValueError("a cache's buffer is a contiguous uint8 tensor")
+
+    @property
+    def n_b(self) -> int:
+        return -(-self.shape.cap // self.shape.block_len)
+
+    def layer(self, l: int) -> "KvCache":
+        """The part of layer l as a cache of its own (the same memory)."""
+        s = self.shape
+        if not 0 <= l < s.L:
+            raise IndexError(l)
+        n = milo_kv_cache_size(s) // s.L
+        one = milo_kv_shape(1, s.S, s.H, s.cap, s.d, s.block_len, s.dtype)
+        return KvCache(one, self.buf[l * n:(l + 1) * n])
+
+
+def milo_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, start: torch.Tensor, count=None,
+                   stream=None) -> None:
+    """Quantise k, v [L][S][H][n][d] (fp32 or bf16; any strides that k and v
+    share, d contiguous) into rows start[s] .. of every session; count int32
+    [S]: only the first count[s] tokens."""
+    c = cache.shape
+    if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 5 or \
+            tuple(k.shape[:3]) != (c.L, c.S, c.H) or k.shape[4] != c.d:
+        raise ValueError(f"k, v: [{c.L}][{c.S}][{c.H}][n][{c.d}] expected, got {tuple(k.shape)} and {tuple(v.shape)}")
+    st = k.stride()
+    if k.numel() and (st != v.stride() or st[4] != 1):
+        raise ValueError("k and v: equal strides and contiguous rows expected")
+    s = _on(k, stream)
+    _int32(start, (c.S,), "start")
+    if count is not None:
+        _int32(count, (c.S,), "count")
+    _same_device(k.device, v, start, count, cache.buf)
+    strides = None if k.is_contiguous() else (ctypes.c_int64 * 4)(*st[:4])
+    rc = lib().milo_kv_append(c, cache.buf.data_ptr(), cache.buf.numel(), k.data_ptr(), v.data_ptr(),
+                              _dtype_code(k.dtype), strides, k.shape[3], start.data_ptr(),
+                              None if count is None else count.data_ptr(), s)
+    _check(rc, "milo_kv_append")
+
+
+def milo_kv_read(cache: KvCache, start: torch.Tensor, n: int, count=None, k_out=None, v_out=None,
+                 out_dtype=torch.float32, stream=None):
+    """(k, v) [L][S][H][n][d]: rows start[s] .. start[s] + n - 1 as values.
+    With count, rows behind count[s] are left as they were in k_out / v_out."""
+    c = cache.shape
+    shape = (c.L, c.S, c.H, n, c.d)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=out_dtype, device=cache.buf.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=k_out.dtype, device=cache.buf.device)
+    for t in (k_out, v_out):
+        if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype != k_out.dtype:
+            raise ValueError(f"k_out, v_out: contiguous {shape} of one type expected, got {t.dtype} {tuple(t.shape)}")
+    s = _on(k_out, stream)
+    _int32(start, (c.S,), "start")
+    if count is not None:
+        _int32(count, (c.S,), "count")
+    _same_device(k_out.device, v_out, start, count, cache.buf)
+    rc = lib().milo_kv_read(c, cache.buf.data_ptr(), cache.buf.numel(), n, start.data_ptr(),
+                            None if count is None else count.data_ptr(), k_out.data_ptr(), v_out.data_ptr(),
+                            _dtype_code(k_out.dtype), s)
+    _used_on(stream, k_out, v_out)
+    _check(rc, "milo_kv_read")
+    return k_out, v_out
+
+
+def _kv_queries(cache: KvCache, q: torch.Tensor, length: torch.Tensor):
+    """(n_q, Hq) of q [L][S][n_q][Hq][d] or [L][S][Hq][d]."""
+    c = cache.shape
+    if q.dim() not in (4, 5) or tuple(q.shape[:2]) != (c.L, c.S) or q.shape[-1] != c.d or not q.is_contiguous():
+        raise ValueError(f"q: contiguous [{c.L}][{c.S}]([n_q])[Hq][{c.d}] expected, got {tuple(q.shape)}")
+    _int32(length, (c.S,), "length")
+    return (q.shape[2] if q.dim() == 5 else 1), q.shape[-2]
+
+
+def milo_kv_select(cache: KvCache, q: torch.Tensor, length: torch.Tensor, n_sel: int, n_first: int = 0,
+                   n_last: int = 1, selected=None, scores=None, return_scores: bool = False, workspace=None,
+                   stream=None):
+    """Blocks of the cache picked by each query: int32 [L][S](n_q)[H][n_sel] ids,
+    ascending, -1 behind the last; with return_scores also the fp32 scores
+    [L][S](n_q)[H][n_b] (-inf: not a candidate)."""
+    c = cache.shape
+    n_q, Hq = _kv_queries(cache, q, length)
+    lead = (c.L, c.S, n_q, c.H) if q.dim() == 5 else (c.L, c.S, c.H)
+    s = _on(q, stream)
+    if selected is None:
+        selected = torch.empty(lead + (n_sel,), dtype=torch.int32, device=q.device)
+    _int32(selected, lead + (n_sel,), "selected")
+    if scores is None and return_scores:
+        scores = torch.empty(lead + (cache.n_b,), dtype=torch.float32, device=q.device)
+    if scores is not None and (scores.dtype != torch.float32 or tuple(scores.shape) != lead + (cache.n_b,) or
+                               not scores.is_contiguous()):
+        raise ValueError(f"scores: contiguous float32 {lead + (cache.n_b,)} expected")
+    if workspace is None:
+        workspace = _bytes(lib().milo_kv_select_workspace_size(c, n_q), q.device)
+    _same_device(q.device, length, selected, scores, workspace, cache.buf)
+    rc = lib().milo_kv_select(c, cache.buf.data_ptr(), cache.buf.numel(), q.data_ptr(), _dtype_code(q.dtype), n_q, Hq,
+                              length.data_ptr(), n_sel, n_first, n_last, selected.data_ptr(),
+                              None if scores is None else scores.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                              s)
+    _used_on(stream, selected, scores, workspace)
+    _check(rc, "milo_kv_select")
+    return (selected, scores) if return_scores else selected
+
+
+def milo_kv_attn_workspace_size(shape: milo_kv_shape, n_q: int, Hq: int, n_sel: int = 0) -> int:
+    return lib().milo_kv_attn_workspace_size(ctypes.byref(shape), n_q, Hq, n_sel)
+
+
+def milo_kv_attn(cache: KvCache, q: torch.Tensor, length: torch.Tensor, selected=None, scale: float = 0.0, out=None,
+                 return_lse: bool = False, workspace=None, stream=None):
+    """GQA attention of q [L][S](n_q)[Hq][d] (fp32 or bf16) over the cached
+    tokens that each query sees, or those of the blocks in `selected`
+    [L][S](n_q)[H][n_sel]; with return_lse also the fp32 log-sum-exp."""
+    c = cache.shape
+    n_q, Hq = _kv_queries(cache, q, length)
+    s = _on(q, stream)
+    n_sel = 0
+    if selected is not None:
+        n_sel = selected.shape[-1]
+        _int32(selected, tuple(q.shape[:-2]) + (c.H, n_sel), "selected")
+    if out is None:
+        out = torch.empty_like(q)
+    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out: like q expected")
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if return_lse else None
+    if workspace is None:
+        workspace = _bytes(lib().milo_kv_attn_workspace_size(c, n_q, Hq, n_sel), q.device)
+    _same_device(q.device, length, selected, out, workspace, cache.buf)
+    rc = lib().milo_kv_attn(c, cache.buf.data_ptr(), cache.buf.numel(), q.data_ptr(), _dtype_code(q.dtype), n_q, Hq,
+                            length.data_ptr(), None if selected is None else selected.data_ptr(), n_sel, scale,
+                            out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+                            workspace.numel(), s)
+    _used_on(stream, out, lse, workspace)
+    _check(rc, "milo_kv_attn")
+    return (out, lse) if return_lse else out
+
+
+def milo_decode_attn_kv(f: Factors, q: torch.Tensor, selected: torch.Tensor, cache: KvCache, length: torch.Tensor,
+                        kv_selected=None, positions=None, rope_base=1e6, out=None, workspace=None, stream=None):
+    """milo_decode_attn_tail with the recent tokens in a quantised cache: q
+    [L][S][Hq][d] fp32, length int32 [S] tokens held, kv_selected int32
+    [L][S][H][kv_n_sel] blocks of the cache (None: all its tokens)."""
+    c = cache.shape
+    if q.dtype != torch.float32 or q.dim() != 4:
+        raise ValueError("q: float32 [L][S][Hq][d] expected")
+    _, Hq = _kv_queries(cache, q, length)
+    s = _on(q, stream)
+    _int32(selected, (c.S, selected.shape[-1]), "selected")
+    if positions is not None:
+        _int32(positions, selected.shape, "positions")
+    kv_n_sel = 0
+    if kv_selected is not None:
+        kv_n_sel = kv_selected.shape[-1]
+        _int32(kv_selected, (c.L, c.S, c.H, kv_n_sel), "kv_selected")
+    if out is None:
+        out = torch.empty_like(q)
+    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out: like q expected")
+    n_sel = selected.shape[-1]
+    if workspace is None:
+        workspace = _bytes(lib().milo_decode_kv_workspace_size(f.handle, c.S, Hq, n_sel, c, kv_n_sel), q.device)
+    _same_device(q.device, length, selected, positions, kv_selected, out, workspace, cache.buf)
+    rc = lib().milo_decode_attn_kv(f.handle, q.data_ptr(), c.S, Hq, selected.data_ptr(),
+                                   None if positions is None else positions.data_ptr(), n_sel, float(rope_base), c,
+                                   cache.buf.data_ptr(), cache.buf.numel(), length.data_ptr(),
+                                   None if kv_selected is None else kv_selected.data_ptr(), kv_n_sel, out.data_ptr(),
+                                   workspace.data_ptr(), workspace.numel(), s)
+    _used_on(stream, out, workspace)
+    _check(rc, "milo_decode_attn_kv")
     return out
 
 

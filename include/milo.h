@@ -32,7 +32,7 @@
  *     the device that ran out) set bits
  *     of a per-device status word that milo_get_status reads and clears.
  *   - No C++ exception crosses this interface.
- *   - d (head dimension) must be 128.
+ *   - d (head dimension) must be 128, except in milo_rope.
  */
 #ifndef MILO_H_
 #define MILO_H_
@@ -60,8 +60,11 @@ typedef enum {
 } milo_status;
 
 /* MILO_INT2: factor codes only (A_b in 2 bits per element, B_b in INT8; see
- * the arena layout below). */
-typedef enum { MILO_F32 = 0, MILO_BF16 = 1, MILO_INT8 = 2, MILO_INT2 = 3 } milo_dtype;
+ * the arena layout below).  MILO_INT4 and MILO_FP8 (e4m3): codes of the
+ * quantised cache of recent tokens only (milo_kv_shape). */
+typedef enum {
+    MILO_F32 = 0, MILO_BF16 = 1, MILO_INT8 = 2, MILO_INT2 = 3, MILO_INT4 = 4, MILO_FP8 = 5
+} milo_dtype;
 
 /* A KV cache of one kind: [L][H][T][d] row-major (d contiguous). */
 typedef struct {
@@ -349,6 +352,227 @@ milo_status milo_bm25_select(const int32_t *blk_ptr, const int32_t *blk_term, co
                              double beta, int32_t n_sel, int32_t *selected, double *scores, void *workspace,
                              size_t ws_bytes, milo_stream_t stream);
 
+/* ---------------------------------------------------------------- rotary */
+
+/* How the angles of milo_rope are scaled for contexts longer than the model
+ * was trained on.  With rd rotated channels, pair i in [0, rd/2) of a token at
+ * position p turns by p * w_i, where w_i is
+ *   NONE    t_i = base^(-2i/rd)
+ *   LINEAR  t_i / factor                                  (position interpolation)
+ *   NTK     t_i with base * factor^(rd/(rd-2))            (needs rd > 2)
+ *   YARN    t_i / factor * g_i + t_i * (1 - g_i), g_i = clamp((i - lo)/(hi - lo), 0, 1),
+ *           lo = max(floor(c(beta_fast)), 0), hi = min(ceil(c(beta_slow)), rd - 1) (hi - lo
+ *           at least 0.001), c(n) = rd ln(orig_ctx / (2 pi n)) / (2 ln base)
+ *   BANDS   with n = orig_ctx t_i / (2 pi) turns over the trained context and
+ *           u = clamp((n - low_freq) / (high_freq - low_freq), 0, 1):
+ *           (1 - u) t_i / factor + u t_i */
+typedef enum {
+    MILO_ROPE_NONE = 0, MILO_ROPE_LINEAR = 1, MILO_ROPE_NTK = 2, MILO_ROPE_YARN = 3, MILO_ROPE_BANDS = 4
+} milo_rope_scaling;
+
+/* Largest head dimension milo_rope takes. */
+#define MILO_ROPE_MAX_D 512
+
+typedef struct {
+    int32_t d;             /* head dimension: even, 2 .. MILO_ROPE_MAX_D               */
+    int32_t rotary_dim;    /* the first rotary_dim channels turn (even, 2 .. d); 0 = d;
+                              the others are copied                                    */
+    int32_t interleaved;   /* 0: pairs (i, i + rd/2); 1: pairs (2i, 2i + 1)            */
+    int32_t scaling;       /* milo_rope_scaling                                        */
+    double base;           /* > 1                                                      */
+    double factor;         /* LINEAR, NTK, YARN, BANDS: > 0                            */
+    double orig_ctx;       /* YARN, BANDS: trained context length, > 0                 */
+    double beta_fast;      /* YARN: 0 < beta_slow <= beta_fast (32 and 1 are usual)    */
+    double beta_slow;
+    double low_freq;       /* BANDS: low_freq < high_freq (1 and 4 are usual)          */
+    double high_freq;
+    double attn_factor;    /* the turned channels are multiplied by this; 0 = 1, and
+                              for YARN 0 = 0.1 ln(factor) + 1                          */
+} milo_rope_params;
+
+/* Fill params: the given d and base, everything turned in half layout, no
+ * scaling (factor 1, orig_ctx 0, beta 32 / 1, freq 1 / 4, attn_factor 0). */
+void milo_rope_default_params(milo_rope_params *params, int32_t d, double base);
+
+/* The angles per position w_i (host, rotary_dim / 2 values, or NULL) and the
+ * factor on the turned channels (host, or NULL).  Errors as milo_rope. */
+milo_status milo_rope_freqs(const milo_rope_params *params, double *w, double *attn_factor);
+
+/*
+ * Rotary positions: y[t][h] = x[t][h] with its pairs (a, b) turned to
+ * (a cos - b sin, a sin + b cos) at the angle positions[t % n_pos] * w_i.
+ * The queries that milo_decode_attn and milo_kv_attn take, and the keys of
+ * recent tokens, are turned like this.  The angle is reduced in fp64, so far
+ * positions lose nothing; the products are fp32, rounded once to y's type.
+ *   x, y:     device, n_tokens x n_heads rows of d values (d contiguous) in
+ *             x_dtype / y_dtype (MILO_F32 or MILO_BF16); row (t, h) starts at
+ *             element t * token_stride + h * head_stride.  Strides of x are >= 0
+ *             (0 reads a broadcast row); rows of y must not overlap.  y may be x
+ *             (same type and strides); any other overlap is an error.
+ *   positions:device, int32 [n_pos], any sign; n_pos >= 1 (n_tokens tokens of
+ *             several layers can share one list)
+ *   transpose:nonzero: the transposed map, i.e. the gradient with respect to x
+ *             of a gradient with respect to y (angles negated, same factor)
+ * n_tokens or n_heads of 0 does nothing.  MILO_ERR_UNSUPPORTED for another
+ * type or d above MILO_ROPE_MAX_D.
+ */
+milo_status milo_rope(const milo_rope_params *params, const void *x, milo_dtype x_dtype, int64_t x_token_stride,
+                      int64_t x_head_stride, void *y, milo_dtype y_dtype, int64_t y_token_stride,
+                      int64_t y_head_stride, const int32_t *positions, int64_t n_pos, int64_t n_tokens,
+                      int32_t n_heads, int32_t transpose, milo_stream_t stream);
+
+/* ------------------------------------------- quantised recent-token cache */
+
+/*
+ * A cache of each session's uncompressed tokens (the question, the tokens
+ * generated so far, or a whole context that is not compressed), quantised
+ * row by row as it is written, with per-block bounds of the keys for
+ * retrieval by query.  Keys are stored as given: already rotated.
+ */
+typedef struct {
+    int32_t L, S, H;     /* layers, sessions, KV heads                              */
+    int32_t cap;         /* tokens a session can hold, 1 .. 2^26                    */
+    int32_t d;           /* head dimension; must be 128                             */
+    int32_t block_len;   /* tokens per block of the retrieval: a multiple of 16,
+                            16 .. 1024; block b holds tokens [b, b + 1) * block_len */
+    milo_dtype dtype;    /* MILO_INT8, MILO_FP8 (e4m3) or MILO_INT4                 */
+} milo_kv_shape;
+
+/*
+ * Cache buffer (device, caller-owned, 256-byte aligned): L layers of
+ * milo_kv_cache_size(shape) / L bytes each, so that the part of one layer is
+ * itself a cache with L = 1.  A layer holds, each section 256-byte aligned
+ * (n_b = ceil(cap / block_len)):
+ *   0  k codes  [S][H][cap][row]      row = 128 bytes, 64 for MILO_INT4
+ *   1  v codes  [S][H][cap][row]
+ *   2  k params [S][H][cap]           float scale; MILO_INT4: fp16 [4][2] (scale, zero)
+ *   3  v params [S][H][cap]
+ *   4  bounds   [S][H][n_b][2][128]   bf16: least and greatest key value per channel
+ *   5  bcodes   [S][H][n_b][2][128]   int8 codes of the bounds
+ *   6  bscale   [S][H][n_b]           float scale of the codes
+ * A row x of 128 values is held as
+ *   INT8  s = max|x| / 127, code = rint(x / s), value = code * s
+ *   FP8   s = max|x| / 448, code = e4m3(x / s), value = code * s
+ *   INT4  per group of 32 channels z = fp16(min), s = fp16((max - min) / 15),
+ *         code = clamp(rint((x - z) / s), 0, 15), value = fp16(code * s + z);
+ *         channel 2j in the low half of byte j
+ * decided in fp32 with the stored parameters, round half to even; a zero scale
+ * has code 0.  The bounds are those of the given keys, rounded outward to bf16;
+ * their codes are rint(bound / s) with s = max|bound| / 127.
+ */
+size_t milo_kv_cache_size(const milo_kv_shape *shape);   /* 0 on an invalid shape */
+
+/* Byte offsets of the seven sections inside a layer (host array of 7). */
+milo_status milo_kv_layout(const milo_kv_shape *shape, size_t *offsets);
+
+/*
+ * Quantise n_new tokens of every session behind the ones it holds: token i of
+ * session s goes to row start[s] + i.
+ *   cache:    cache_bytes >= milo_kv_cache_size
+ *   k, v:     device, in_dtype (MILO_F32 or MILO_BF16), 16-byte aligned, rows of
+ *             128 contiguous values; row (l, s, h, i) starts at element
+ *             l strides[0] + s strides[1] + h strides[2] + i strides[3] (host
+ *             array, multiples of 8, >= 0), or [L][S][H][n_new][d] when strides
+ *             is NULL.  Both with the same strides.
+ *   start:    device, int32 [S], 0 <= start[s]
+ *   count:    device, int32 [S], 0 <= count[s] <= n_new: only the first count[s]
+ *             tokens are written; NULL = n_new
+ * A range outside [0, cap] (or a bad count) sets MILO_ERR_BOUNDS and that
+ * session's rows are left as they were.  Rows outside the ranges are never
+ * touched.  A value that is not finite (MILO_INT4: above 65504 in size) sets
+ * MILO_ERR_NONFINITE and is stored as 0 (as +-65504).
+ * The bounds of a block whose first token is written are those of the written
+ * tokens; a block that is continued keeps what it had (rows written again
+ * widen its bounds, never narrow them), so a session begins at token 0.
+ */
+milo_status milo_kv_append(const milo_kv_shape *shape, void *cache, size_t cache_bytes, const void *k, const void *v,
+                           milo_dtype in_dtype, const int64_t *strides, int32_t n_new, const int32_t *start,
+                           const int32_t *count, milo_stream_t stream);
+
+/*
+ * Read rows start[s] .. start[s] + n - 1 of every session back as values:
+ * k_out, v_out [L][S][H][n][d] (device, 16-byte aligned, out_dtype MILO_F32 or
+ * MILO_BF16; either may be NULL).  start, count and their errors as in
+ * milo_kv_append; rows behind count[s] are left as they were.
+ */
+milo_status milo_kv_read(const milo_kv_shape *shape, const void *cache, size_t cache_bytes, int32_t n,
+                         const int32_t *start, const int32_t *count, void *k_out, void *v_out, milo_dtype out_dtype,
+                         milo_stream_t stream);
+
+/* Bytes of scratch milo_kv_select needs (0 on invalid input). */
+size_t milo_kv_select_workspace_size(const milo_kv_shape *shape, int32_t n_q);
+
+/*
+ * Retrieval by query: the n_sel blocks of the cache with the greatest upper
+ * bound of q . k, per layer, session, query and KV head.  The query-vector
+ * counterpart of milo_bm25_select, for the cache of recent tokens.  Query i of
+ * session s sees the tokens t <= len[s] - n_q + i (the last n_q tokens held are
+ * the queries' own); blocks that begin behind that are not candidates.  With
+ * the query's INT8 codes c_j = rint(q_j / u), u = max|q| / 127, and the
+ * block's bound codes lo_j, hi_j with scale s, a query head's bound is
+ *   (sum_j max(c_j lo_j, c_j hi_j)) * u        (the sum exact in integers)
+ * and the block's score the greatest over the G = Hq / H query heads of the KV
+ * head, times s.
+ *   q:        device, q_dtype (MILO_F32 or MILO_BF16), [L][S][n_q][Hq][d], 16-byte aligned
+ *   len:      device, int32 [S], tokens held; outside [0, cap] sets
+ *             MILO_ERR_BOUNDS and counts as 0
+ *   n_sel:    1 .. n_b, of which the first n_first and the last n_last candidates
+ *             are always taken (n_first + n_last <= n_sel)
+ *   selected: device, int32 [L][S][n_q][H][n_sel] out: block ids ascending, -1
+ *             behind the last when there are fewer candidates; ties in score
+ *             go to the lower id
+ *   scores:   device, float [L][S][n_q][H][n_b] out (-inf: no candidate), or NULL
+ * A q that is not finite sets MILO_ERR_NONFINITE and counts as 0 there.
+ */
+milo_status milo_kv_select(const milo_kv_shape *shape, const void *cache, size_t cache_bytes, const void *q,
+                           milo_dtype q_dtype, int32_t n_q, int32_t Hq, const int32_t *len, int32_t n_sel,
+                           int32_t n_first, int32_t n_last, int32_t *selected, float *scores, void *workspace,
+                           size_t ws_bytes, milo_stream_t stream);
+
+/* Bytes of scratch milo_kv_attn needs (0 on invalid input); n_sel = 0: dense. */
+size_t milo_kv_attn_workspace_size(const milo_kv_shape *shape, int32_t n_q, int32_t Hq, int32_t n_sel);
+
+/*
+ * GQA attention over the cache: for query i of session s, the softmax over the
+ * tokens t <= len[s] - n_q + i (the last n_q tokens held are the queries'
+ * own) of scale * q . k_t, times v_t; with `selected`, over the tokens of the
+ * selected blocks alone.
+ *   q, out:   device, q_dtype (MILO_F32 or MILO_BF16), [L][S][n_q][Hq][d], 16-byte
+ *             aligned; q already rotated.  Products and sums are held to fp32 for
+ *             MILO_F32; MILO_BF16 rounds the softmax weights to fp16.
+ *   len:      as milo_kv_select
+ *   selected: device, int32 [L][S][n_q][H][n_sel] block ids (as milo_kv_select
+ *             writes them; any order), -1 = none, or NULL for all tokens (n_sel =
+ *             0).  An id listed twice counts twice; another id outside [0, n_b)
+ *             sets MILO_ERR_BOUNDS and contributes nothing.
+ *   scale:    > 0, or 0 for 1 / sqrt(d)
+ *   lse:      device, float [L][S][n_q][Hq] out: the logarithm of the sum of
+ *             exp(scale * q . k_t), to merge with other parts, or NULL
+ * A query that sees no token gets zeros, and -inf as lse; one that is not
+ * finite gets values that are not, in its own row alone.
+ */
+milo_status milo_kv_attn(const milo_kv_shape *shape, const void *cache, size_t cache_bytes, const void *q,
+                         milo_dtype q_dtype, int32_t n_q, int32_t Hq, const int32_t *len, const int32_t *selected,
+                         int32_t n_sel, double scale, void *out, float *lse, void *workspace, size_t ws_bytes,
+                         milo_stream_t stream);
+
+/* Bytes of scratch milo_decode_attn_kv needs (0 on invalid input). */
+size_t milo_decode_kv_workspace_size(const milo_factors *f, int32_t S, int32_t Hq, int32_t n_sel,
+                                     const milo_kv_shape *shape, int32_t kv_n_sel);
+
+/*
+ * milo_decode_attn_tail with the recent tokens in a quantised cache: the
+ * softmax over the selected compressed blocks' tokens and the session's cached
+ * tokens t < len[s], all of them or (kv_selected not NULL) those of the blocks
+ * kv_selected [L][S][H][kv_n_sel] of the cache, as milo_kv_attn with n_q = 1 and
+ * scale 1 / sqrt(d).  shape's L, S, H and d are the call's.  An empty cache for
+ * every session gives milo_decode_attn's output bit for bit.
+ */
+milo_status milo_decode_attn_kv(const milo_factors *f, const float *q, int32_t S, int32_t Hq, const int32_t *selected,
+                                const int32_t *positions, int32_t n_sel, double rope_base, const milo_kv_shape *shape,
+                                const void *cache, size_t cache_bytes, const int32_t *len, const int32_t *kv_selected,
+                                int32_t kv_n_sel, float *out, void *workspace, size_t ws_bytes, milo_stream_t stream);
+
 /* ------------------------------------------------------ factor handles */
 
 /* Views (device pointers into the arena) of one kind (0 = K, 1 = V).  Any
@@ -415,7 +639,12 @@ typedef enum {
     MILO_TK_TAIL = 8,        /* attention over the recent uncompressed tokens (k_tail_attn) */
     MILO_TK_STAGE = 9,       /* host-resident factors of the selected blocks staged on the device */
     MILO_TK_RETRIEVE = 10,   /* BM25 block scores and the per-session top blocks */
-    MILO_TK_COUNT = 11
+    MILO_TK_ROPE = 11,       /* rotary positions (milo_rope) */
+    MILO_TK_KV_WRITE = 12,   /* rows quantised into the recent-token cache, and block bounds */
+    MILO_TK_KV_READ = 13,    /* rows of that cache read back as values */
+    MILO_TK_KV_SELECT = 14,  /* block scores by query and the top blocks */
+    MILO_TK_KV_ATTN = 15,    /* attention over that cache, and the merge of its parts */
+    MILO_TK_COUNT = 16
 } milo_timed_stage;
 
 /* on != 0: start recording (previous records are dropped); on == 0: stop.
@@ -425,7 +654,7 @@ milo_status milo_timing_enable(int32_t on);
 /* Wait for every recorded event, then write per stage (n entries, stage
  * order above; n <= MILO_TK_COUNT) the summed milliseconds into ms and the
  * number of bracketed launches into count, and drop the records.  ms and
- * count are host arrays.  MILO_ERR_INVALID_ARG for n outside 0 .. 8 or a NULL
+ * count are host arrays.  MILO_ERR_INVALID_ARG for n outside 0 .. MILO_TK_COUNT or a NULL
  * array; a CUDA error of the event queries is returned as MILO_ERR_CUDA. */
 milo_status milo_timing_read(double *ms, int64_t *count, int32_t n);
 

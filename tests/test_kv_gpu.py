@@ -1,0 +1,690 @@
+"""Rotary positions and the quantised cache of recent tokens on the GPU,
+against the plain forms of tests/kv_reference.py.
+
+Tolerances are counted from roundings where they are used; codes, bounds and
+selections have to be equal."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from block_wise_rank_b200 import build as milo_build
+from block_wise_rank_b200 import milo, synth
+from tests import kv_reference as R
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+HALF_STEP = {BF: 2.0 ** -8, F32: 2.0 ** -24}     # finfo.eps / 2
+KINDS = ["int8", "fp8", "int4"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    milo_build.build()
+    milo.lib()
+    assert torch.cuda.is_available()
+    milo.milo_get_status()
+
+
+def ok(status=milo.MILO_OK):
+    assert milo.milo_get_status() == status
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def rnd(seed, *shape, dtype=F32, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(dtype).cuda()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+# ------------------------------------------------------------------ rotary
+# a turn's error relative to |a| + |b|: the reduced argument (pi 2^-25), sincospi (1 ulp: 2^-23), the factor's own
+# rounding and its product (2^-23), two products and a sum (3 2^-24)
+TURN = 2.0 ** -23 * (0.8 + 1 + 1 + 1.5)
+
+
+def check_rope(x, pos, y, p, ref_w, inter=False, m=1.0, transpose=False, extra=0.0):
+    rd = 2 * len(ref_w)
+    ref = R.rope(np64(x), pos, ref_w, inter, m, transpose)
+    size = R.rope_pair_size(np64(x), rd, inter)
+    tol = (TURN + extra) * m * size + HALF_STEP[y.dtype] * np.abs(ref) * (1 + 2.0 ** -7) * (size > 0)
+    if y.dtype != x.dtype and y.dtype == BF:     # channels that do not turn are rounded as well
+        tol = tol + (size == 0) * HALF_STEP[BF] * np.abs(ref)
+    assert np.all(np.abs(np64(y) - ref) <= tol), np.max(np.abs(np64(y) - ref) - tol)
+
+
+SCALINGS = [("none", {}), ("linear", dict(factor=4.0)), ("ntk", dict(factor=2.5)),
+            ("yarn", dict(factor=4.0, orig_ctx=4096)), ("bands", dict(factor=8.0, orig_ctx=8192))]
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("xd,yd", [(BF, BF), (F32, F32), (BF, F32), (F32, BF)])
+@pytest.mark.parametrize("nt,nh,d,rd", [(1, 1, 128, 0), (5, 3, 128, 128), (33, 4, 80, 20), (7, 2, 6, 4), (3, 1, 2, 2),
+                                        (2, 40, 512, 64), (300, 5, 96, 40), (1000, 28, 128, 128)])
+def test_rope_types_and_sizes(inter, xd, yd, nt, nh, d, rd):
+    for k, (scaling, kw) in enumerate(SCALINGS):
+        if scaling == "ntk" and (rd or d) <= 2:
+            continue
+        x = rnd(nt * d + k, nt, nh, d, dtype=xd)
+        pos = (np.arange(nt) * 37 + 11 * k).astype(np.int32)
+        p = milo.rope_params(d, 1e4, rotary_dim=rd, interleaved=inter, scaling=scaling, **kw)
+        m = 0.1 * math.log(kw["factor"]) + 1 if scaling == "yarn" else 1.0
+        w = R.rope_freqs(rd or d, 1e4, scaling, **kw)
+        for back in (False, True):
+            y = milo.milo_rope(x, i32(pos.tolist()), p, out_dtype=yd, transpose=back)
+            check_rope(x, pos, y, p, w, inter, m, back)
+    ok()
+
+
+def test_rope_far_and_negative_positions():
+    pos = [2 ** 31 - 1, -2 ** 31, -1, 2 ** 24 + 1, 0]
+    x = rnd(1, 5, 2, 128)
+    p = milo.rope_params(128, 1e6)
+    y = milo.milo_rope(x, i32(pos), p)
+    # turns of at most 2^28.4, each of two factors rounded to 2^-53, and their product: 3 * 2^-24.6 turns
+    check_rope(x, pos, y, p, R.rope_freqs(128, 1e6), extra=3 * 2.0 ** -24.6 * 2 * math.pi)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_rope_strides_alignment_and_in_place(inter, dt):
+    p = milo.rope_params(64, 1e4, rotary_dim=32, interleaved=inter)
+    w = R.rope_freqs(32, 1e4)
+    pos = list(range(3, 14))
+    packed = rnd(5, 11, 7 * 64 + 3, dtype=dt)                      # odd row length: element-wise accesses
+    for off in (0, 1, 8):
+        x = packed[:, off:off + 5 * 64].view(11, 5, 64) if off == 8 else packed[:, off:off + 320].unflatten(1, (5, 64))
+        y = milo.milo_rope(x, i32(pos), p)
+        check_rope(x, pos, y, p, w, inter)
+    heads_first = rnd(6, 5, 11, 64, dtype=dt).transpose(0, 1)     # [H][T][d] storage
+    out = torch.full((5, 11, 64), 7.0, dtype=dt, device="cuda").transpose(0, 1)
+    milo.milo_rope(heads_first, i32(pos), p, out=out)
+    check_rope(heads_first, pos, out, p, w, inter)
+    row = rnd(7, 1, 1, 64, dtype=dt)
+    y = milo.milo_rope(row.expand(11, 5, 64), i32(pos), p)        # one row, broadcast
+    check_rope(row.expand(11, 5, 64), pos, y, p, w, inter)
+    big = rnd(8, 11, 9, 64, dtype=dt)
+    keep = big.clone()
+    milo.milo_rope(big[:, 2:7], i32(pos), p, out=big[:, 2:7])     # in place in a packed row: the others stay
+    check_rope(keep[:, 2:7], pos, big[:, 2:7], p, w, inter)
+    assert torch.equal(big[:, :2], keep[:, :2]) and torch.equal(big[:, 7:], keep[:, 7:])
+    with pytest.raises(milo.MiloError):
+        milo.milo_rope(big[:, 0:5], i32(pos), p, out=big[:, 2:7])
+    e = milo.milo_rope(big[:0], i32(pos), p)
+    assert e.shape == (0, 9, 64)
+
+
+def test_rope_positions_repeat_over_layers():
+    x = rnd(9, 12, 2, 128)
+    pos = [5, 0, 900]
+    p = milo.rope_params(128)
+    check_rope(x, pos, milo.milo_rope(x, i32(pos), p), p, R.rope_freqs(128, 1e6))
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_gradient(inter):
+    """Against the formula (the transposed map) and against differences of the forward pass."""
+    p = milo.rope_params(48, 100.0, rotary_dim=36, interleaved=inter, scaling="yarn", factor=4.0, orig_ctx=64)
+    pos = i32([0, 1, 17, 5000])
+    x, dy = rnd(10, 4, 3, 48), rnd(11, 4, 3, 48)
+    dx = milo.milo_rope(dy, pos, p, transpose=True)
+    check_rope(dy, pos.cpu().numpy(), dx, p, R.rope_freqs(36, 100.0, "yarn", factor=4.0, orig_ctx=64), inter,
+               0.1 * math.log(4) + 1, True)
+    # the map is linear: <R(x + h e) - R(x), dy> / h = dx . e for any step h; here h = 1 and e = a random direction
+    e = rnd(12, 4, 3, 48)
+    f = (milo.milo_rope(x + e, pos, p).double() - milo.milo_rope(x, pos, p).double())
+    lhs, rhs = float((f * dy.double()).sum()), float((dx.double() * e.double()).sum())
+    # 576 values with pairs of size at most 2 max: each side's roundings
+    n = 576 * (2 * TURN * 1.14 + 2.0 ** -22) * 2 * float((x.abs().max() + e.abs().max()) * dy.abs().max())
+    assert abs(lhs - rhs) <= n
+
+
+# ------------------------------------------------------------------- cache
+def make(L, S, H, cap, bl, dtype, fill=0xFF):
+    """A cache whose untouched bytes are NaN scales, NaN e4m3 codes and infinite zeros."""
+    c = milo.KvCache(milo.kv_shape(L, S, H, cap, bl, dtype))
+    c.buf.fill_(fill)
+    return c
+
+
+def sections(c):
+    """The cache's sections as numpy arrays over all layers (codes as numbers)."""
+    s, o = c.shape, milo.milo_kv_layout(c.shape)
+    layer = milo.milo_kv_cache_size(s) // s.L
+    raw = c.buf[:s.L * layer].cpu().numpy().reshape(s.L, layer)
+    kind = {v: k for k, v in milo.KV_DTYPES.items()}[s.dtype]
+    row, par = (64, 16) if kind == "int4" else (128, 4)
+    rows, n_b = s.S * s.H * s.cap, c.n_b
+    got = {}
+    for i, name in ((0, "k"), (1, "v")):
+        b = np.ascontiguousarray(raw[:, o[i]:o[i] + rows * row]).reshape(s.L, s.S, s.H, s.cap, row)
+        if kind == "int4":
+            got[name] = np.stack([b & 15, b >> 4], -1).reshape(s.L, s.S, s.H, s.cap, 128).astype(np.float64)
+        elif kind == "int8":
+            got[name] = b.view(np.int8).astype(np.float64)
+        else:
+            got[name] = torch.from_numpy(b).view(torch.float8_e4m3fn).double().numpy()
+        p = np.ascontiguousarray(raw[:, o[2 + i]:o[2 + i] + rows * par])
+        got[name + "p"] = p.view(np.float16).reshape(s.L, s.S, s.H, s.cap, 4, 2) if kind == "int4" else \
+            p.view(np.float32).reshape(s.L, s.S, s.H, s.cap)
+    nb = s.S * s.H * n_b
+    b = np.ascontiguousarray(raw[:, o[4]:o[4] + nb * 512]).view(np.uint16).astype(np.uint32) << 16
+    got["bounds"] = b.view(np.float32).reshape(s.L, s.S, s.H, n_b, 2, 128)
+    got["codes"] = np.ascontiguousarray(raw[:, o[5]:o[5] + nb * 256]).view(np.int8).reshape(s.L, s.S, s.H, n_b, 2, 128)
+    got["scale"] = np.ascontiguousarray(raw[:, o[6]:o[6] + nb * 4]).view(np.float32).reshape(s.L, s.S, s.H, n_b)
+    return got, kind
+
+
+def append(c, k, v, start, count=None):
+    milo.milo_kv_append(c, k, v, i32(start), None if count is None else i32(count))
+
+
+def f32np(t):
+    return t.float().cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("bl", [16, 48, 64])
+def test_append_codes_bounds_and_untouched_bytes(dtype, dt, bl):
+    L, S, H, cap, n = 2, 4, 3, 150, 70
+    c = make(L, S, H, cap, bl, dtype)
+    before, _ = sections(c)
+    k, v = rnd(1, L, S, H, n, 128, dtype=dt, scale=3.0), rnd(2, L, S, H, n, 128, dtype=dt)
+    k[0, 0, 0, 0] = 0.0                                         # a row of zeros
+    k[0, 0, 0, 1] = 2.5                                         # a constant row
+    k[0, 0, 1, 2, 5:] = 1e-30
+    v[1, 1, 1, 3] *= 1e4
+    start, count = [0, 80, 33, 7], [70, 70, 1, 0]
+    append(c, k, v, start, count)
+    ok()
+    got, _ = sections(c)
+    kn, vn = f32np(k), f32np(v)
+    touched = np.zeros((S, cap), bool)
+    for s in range(S):
+        touched[s, start[s]:start[s] + count[s]] = True
+        for name, x in (("k", kn), ("v", vn)):
+            q, p = R.quantise(x[:, s, :, :count[s]], dtype)
+            rows = slice(start[s], start[s] + count[s])
+            np.testing.assert_array_equal(got[name][:, s, :, rows], q)
+            np.testing.assert_array_equal(got[name + "p"][:, s, :, rows], p)
+    for name in ("k", "v", "kp", "vp"):                         # the others are as they were
+        a, b = np.moveaxis(got[name], 2, 1)[:, :, ~touched], np.moveaxis(before[name], 2, 1)[:, :, ~touched]
+        assert a.tobytes() == b.tobytes()
+    for s in range(S):
+        for b in range(c.n_b):
+            t = np.arange(max(b * bl, start[s]), min((b + 1) * bl, start[s] + count[s]))
+            if not t.size:
+                assert got["bounds"][:, s, :, b].tobytes() == before["bounds"][:, s, :, b].tobytes()
+                assert got["codes"][:, s, :, b].tobytes() == before["codes"][:, s, :, b].tobytes()
+            elif start[s] <= b * bl:                            # begun here: the bounds of these rows alone
+                x = kn[:, s, :, t - start[s]]
+                x = np.moveaxis(x, 0, 2) if x.shape[0] == t.size else x
+                lo, hi = R.outward(x.min(2), False), R.outward(x.max(2), True)
+                np.testing.assert_array_equal(got["bounds"][:, s, :, b], np.stack([lo, hi], -2))
+                q, p = R.bound_codes(lo, hi)
+                np.testing.assert_array_equal(got["codes"][:, s, :, b], q)
+                np.testing.assert_array_equal(got["scale"][:, s, :, b], p)
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+def test_append_token_by_token_equals_at_once(dtype):
+    L, S, H, cap, bl, n = 1, 2, 2, 70, 32, 67
+    k, v = rnd(3, L, S, H, n, 128), rnd(4, L, S, H, n, 128)
+    a, b = make(L, S, H, cap, bl, dtype), make(L, S, H, cap, bl, dtype)
+    append(a, k, v, [0, 3])
+    append(b, k[:, :, :, :1], v[:, :, :, :1], [0, 3])
+    # session 1 begins inside a block: its bounds go on from what the buffer held; give both the same
+    for t in range(1, n):
+        append(b, k[:, :, :, t:t + 1], v[:, :, :, t:t + 1], [t, t + 3])
+    ok()
+    ga, gb = sections(a)[0], sections(b)[0]
+    for name in ga:
+        x, y = (ga[name][:, :1], gb[name][:, :1]) if name in ("bounds", "codes", "scale") else (ga[name], gb[name])
+        np.testing.assert_array_equal(x, y)
+
+
+def test_append_strides_of_a_packed_projection():
+    L, S, H, n = 2, 3, 2, 19
+    qkv = rnd(5, L, S, n, 12, 128, dtype=BF)                     # [L][S][token][q heads | k heads | v heads][d]
+    k, v = qkv[..., 8:10, :].transpose(2, 3), qkv[..., 10:12, :].transpose(2, 3)
+    a, b = make(L, S, H, 32, 16, "int8"), make(L, S, H, 32, 16, "int8")
+    append(a, k, v, [0, 4, 13])
+    append(b, k.contiguous(), v.contiguous(), [0, 4, 13])
+    ok()
+    assert torch.equal(a.buf, b.buf)
+    one = rnd(6, 1, 1, 1, 1, 128).expand(L, S, H, n, 128)        # one row everywhere: strides of 0
+    append(a, one, one, [0, 0, 0])
+    append(b, one.contiguous(), one.contiguous(), [0, 0, 0])
+    assert torch.equal(a.buf, b.buf)
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+def test_append_bad_ranges_and_values(dtype):
+    L, S, H, cap = 1, 5, 1, 40
+    c = make(L, S, H, cap, 16, dtype)
+    keep = c.buf.clone()
+    k = rnd(7, L, S, H, 8, 128)
+    append(c, k, k, [-1, 33, 2 ** 31 - 1, 0, 0], [8, 8, 8, 9, -1])
+    ok(milo.MILO_ERR_BOUNDS)
+    assert torch.equal(c.buf, keep)
+    ok()
+    k[0, 0, 0, 0, 3], k[0, 0, 0, 1, 4], k[0, 0, 0, 2, 5] = math.nan, math.inf, -math.inf
+    append(c, k, k, [0] * 5)
+    ok(milo.MILO_ERR_NONFINITE)
+    z = f32np(torch.where(torch.isfinite(k), k, 0.0))
+    got, _ = sections(c)
+    q, p = R.quantise(z, dtype)
+    np.testing.assert_array_equal(got["k"][:, :, :, :8], q)
+    np.testing.assert_array_equal(got["vp"][:, :, :, :8], p)
+    x = k.nan_to_num(0, 0, 0)
+    x[0, 0, 0, 0, 0], x[0, 0, 0, 0, 1], x[0, 0, 0, 1, 0] = 1e38, -1e38, 65504.0
+    append(c, x, x, [0] * 5)
+    ok(milo.MILO_ERR_NONFINITE if dtype == "int4" else milo.MILO_OK)
+    z = f32np(x.clamp(-65504, 65504) if dtype == "int4" else x)
+    got, _ = sections(c)
+    np.testing.assert_array_equal(got["k"][:, :, :, :8], R.quantise(z, dtype)[0])
+
+
+def test_append_smallest_and_largest_values():
+    BIG = torch.finfo(F32).max
+    c = make(1, 1, 1, 16, 16, "int8")
+    k = torch.zeros(1, 1, 1, 4, 128, device="cuda")
+    k[..., 0, 0], k[..., 1, 0], k[..., 2, :], k[..., 3, :] = 1e-45, BIG, 1e-39, -BIG
+    append(c, k, k, [0])
+    ok()
+    got, _ = sections(c)
+    q, p = R.quantise(f32np(k), "int8")
+    np.testing.assert_array_equal(got["k"][:, :, :, :4], q)
+    np.testing.assert_array_equal(got["kp"][:, :, :, :4], p)
+    assert np.isfinite(got["bounds"][0, 0, 0, 0]).all()
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+@pytest.mark.parametrize("out", [BF, F32])
+def test_read_back(dtype, out):
+    L, S, H, cap, n = 2, 3, 2, 90, 37
+    c = make(L, S, H, cap, 32, dtype)
+    k, v = rnd(8, L, S, H, cap, 128), rnd(9, L, S, H, cap, 128)
+    append(c, k, v, [0] * 3)
+    start, count = [0, 53, 20], [37, 37, 5]
+    ko, vo = (torch.full((L, S, H, n, 128), 7.0, dtype=out, device="cuda") for _ in range(2))
+    milo.milo_kv_read(c, i32(start), n, i32(count), ko, vo)
+    ok()
+    for x, y in ((k, ko), (v, vo)):
+        q, p = R.quantise(f32np(x), dtype)
+        ref = R.values(q, p, dtype).astype(np.float32)          # one rounding to fp32, as the kernel's product
+        for s in range(S):
+            want = torch.from_numpy(ref[:, s, :, start[s]:start[s] + count[s]]).to(out)
+            assert torch.equal(y[:, s, :, :count[s]].cpu(), want)
+            assert (y[:, s, :, count[s]:] == 7.0).all()
+    keep = ko.clone()
+    milo.milo_kv_read(c, i32([-1, 54, 2 ** 31 - 1]), n, None, ko, vo)
+    ok(milo.MILO_ERR_BOUNDS)
+    assert torch.equal(ko, keep)
+    assert milo.lib().milo_kv_read(c.shape, c.buf.data_ptr(), c.buf.numel(), n, i32(start).data_ptr(), None, None,
+                                   vo.data_ptr(), milo.MILO_BF16 if out == BF else milo.MILO_F32, None) == 0
+    torch.cuda.synchronize()
+
+
+# --------------------------------------------------------------- retrieval
+def seen(length, n_q, i):
+    return max(0, length - n_q + i + 1)
+
+
+@pytest.mark.parametrize("G", [1, 3, 7, 8, 12, 20])
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("bl,cap,n_q", [(16, 16, 1), (16, 1000, 2), (64, 5000, 1), (48, 333, 3)])
+def test_select(G, dt, bl, cap, n_q):
+    L, S, H = 2, 3, 2
+    c = make(L, S, H, cap, bl, "int4")
+    k = rnd(10, L, S, H, cap, 128)
+    append(c, k, k, [0] * S)
+    length = [cap, cap // 3, min(1, cap)]
+    q = rnd(11, L, S, n_q, H * G, 128, dtype=dt)
+    q[0, 0, 0, 0] = 0.0
+    got, _ = sections(c)
+    for n_sel, nf, nl in {(1, 0, 1), (1, 0, 0), (min(9, c.n_b), min(1, c.n_b - 1), 1), (c.n_b, 0, 0)}:
+        sel, sc = milo.milo_kv_select(c, q, i32(length), n_sel, nf, nl, return_scores=True)
+        assert torch.equal(sel, milo.milo_kv_select(c, q, i32(length), n_sel, nf, nl))
+        sel, sc, qn = sel.cpu().numpy(), sc.cpu().numpy(), f32np(q)
+        for l, s, i, h in np.ndindex(L, S, n_q, H):
+            cand = -(-seen(length[s], n_q, i) // bl)
+            ref = R.scores(qn[l, s, i, h * G:(h + 1) * G], got["codes"][l, s, h], got["scale"][l, s, h])
+            np.testing.assert_array_equal(sc[l, s, i, h, :cand], ref[:cand])
+            assert np.all(np.isneginf(sc[l, s, i, h, cand:]))
+            np.testing.assert_array_equal(sel[l, s, i, h], R.top(ref, cand, n_sel, nf, nl))
+    ok()
+
+
+def test_select_ties_lengths_and_bad_queries():
+    L, S, H, cap, bl = 1, 5, 1, 640, 16
+    c = make(L, S, H, cap, bl, "fp8")
+    k = rnd(12, 1, 1, 1, bl, 128).repeat(L, S, H, cap // bl, 1)  # equal blocks: ties go to the lower ids
+    append(c, k, k, [0] * S)
+    q = rnd(13, L, S, 2, 128)
+    sel = milo.milo_kv_select(c, q, i32([640, 0, 17, -3, 641]), 7, 0, 1).cpu().numpy()
+    ok(milo.MILO_ERR_BOUNDS)
+    assert sel[0, 0, 0].tolist() == [0, 1, 2, 3, 4, 5, 39]
+    assert sel[0, 2, 0].tolist() == [0, 1, -1, -1, -1, -1, -1]
+    assert (sel[0, [1, 3, 4]] == -1).all()
+    q[0, 0, 0, 0], q[0, 2, 1, 5] = math.nan, math.inf
+    want = milo.milo_kv_select(c, torch.where(torch.isfinite(q), q, 0.0), i32([640] * S), 3)
+    ok()
+    assert torch.equal(milo.milo_kv_select(c, q, i32([640] * S), 3), want)
+    ok(milo.MILO_ERR_NONFINITE)
+    z = milo.milo_kv_select(c, torch.zeros_like(q), i32([640] * S), 3, 0, 0)
+    assert (z.cpu() == torch.tensor([0, 1, 2])).all()
+
+
+def test_select_negative_and_zero_scores_order():
+    """A block whose keys all point away scores below zero, and -0 ties with +0."""
+    c = make(1, 1, 1, 64, 16, "int8")
+    k = torch.zeros(1, 1, 1, 64, 128, device="cuda")
+    k[..., :16, :], k[..., 16:32, :], k[..., 48:, :] = -1.0, 0.0, -1e-40
+    append(c, k, k, [0])
+    q = torch.ones(1, 1, 1, 128, device="cuda")
+    assert milo.milo_kv_select(c, q, i32([64]), 2, 0, 0).flatten().tolist() == [1, 2]
+    assert milo.milo_kv_select(c, -q, i32([64]), 1, 0, 0).flatten().tolist() == [0]
+
+
+# --------------------------------------------------------------- attention
+def check_attn(c, q, length, sel=None, scale=0.0, out=None, lse=None, status=milo.MILO_OK):
+    """milo_kv_attn against 64 bits on the values that the cache holds."""
+    if out is None:
+        out, lse = milo.milo_kv_attn(c, q, i32(length), None if sel is None else i32(sel), scale, return_lse=True)
+        ok(status)
+    five = q.dim() == 5
+    qn = np64(q if five else q[:, :, None])
+    on = np64(out if five else out[:, :, None])
+    ln = np64(lse if five else lse[:, :, None])
+    got, kind = sections(c)
+    L, S, n_q, Hq, _ = qn.shape
+    H, bl = c.shape.H, c.shape.block_len
+    G = Hq // H
+    sel = None if sel is None else np.asarray(sel).reshape(L, S, n_q, H, -1)
+    scale = scale or 128 ** -0.5
+    for l, s, h in np.ndindex(L, S, H):
+        n = length[s] if 0 <= length[s] <= c.shape.cap else 0
+        k, v = (R.values(got[x][l, s, h, :n], got[x + "p"][l, s, h, :n], kind) for x in ("k", "v"))
+        for i in range(n_q):
+            t = np.arange(seen(n, n_q, i))
+            if sel is not None:
+                b = [x for x in sel[l, s, i, h] if 0 <= x < c.n_b]
+                t = np.concatenate([np.arange(x * bl, min((x + 1) * bl, t.size)) for x in b] + [t[:0]]).astype(int)
+            o, e, err, le = R.attn(qn[l, s, i, h * G:(h + 1) * G], k[t], v[t], scale, q.dtype == BF, HALF_STEP[q.dtype])
+            g = on[l, s, i, h * G:(h + 1) * G]
+            assert np.all(np.abs(g - o) <= err), (l, s, h, i, np.max(np.abs(g - o) / err))
+            w = ln[l, s, i, h * G:(h + 1) * G]
+            if t.size == 0:
+                assert np.all(g == 0) and np.all(np.isneginf(w))
+            else:
+                assert np.all(np.abs(w - e) <= le), (l, s, h, i, np.max(np.abs(w - e) / le))
+
+
+def filled(L, S, H, cap, bl, dtype, length, seed=20, scale=1.0):
+    """A cache that holds length[s] tokens; everything behind them is 0xFF."""
+    c = make(L, S, H, cap, bl, dtype)
+    n = max(1, max(length))
+    k, v = rnd(seed, L, S, H, n, 128, scale=scale), rnd(seed + 1, L, S, H, n, 128)
+    append(c, k, v, [0] * S, [min(x, n) for x in length])
+    ok()
+    return c
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("G,H", [(1, 1), (7, 2), (8, 1), (12, 1), (5, 3)])
+def test_attn_lengths(dtype, dt, G, H):
+    length = [0, 1, 15, 16, 17, 64, 257, 300]
+    c = filled(1, len(length), H, 300, 64, dtype, length)
+    check_attn(c, rnd(21, 1, len(length), H * G, 128, dtype=dt), length)
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("n_q,G", [(2, 1), (3, 7), (17, 4), (40, 2)])
+def test_attn_several_queries(dtype, dt, n_q, G):
+    length = [0, 1, n_q - 1, n_q, 100, 203]
+    c = filled(2, len(length), 2, 203, 16, dtype, length)
+    check_attn(c, rnd(22, 2, len(length), n_q, 2 * G, 128, dtype=dt), length)
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("bl,n_q,G", [(16, 1, 7), (48, 2, 3), (64, 1, 8), (128, 1, 12)])
+def test_attn_selected_blocks(dtype, dt, bl, n_q, G):
+    L, S, H, cap = 2, 4, 2, 700
+    length = [700, 333, 1, 0]
+    c = filled(L, S, H, cap, bl, dtype, length)
+    g = np.random.default_rng(bl)
+    sel = g.integers(-1, c.n_b, (L, S, n_q, H, 5)).astype(np.int32)   # any order, some twice, some none, some unseen
+    sel[0, 0, 0, 0] = -1                                              # nothing selected
+    sel[1, 0, 0, 1] = c.n_b - 1
+    q = rnd(23, L, S, n_q, H * G, 128, dtype=dt)
+    check_attn(c, q, length, sel.tolist())
+    if n_q == 1:
+        check_attn(c, q[:, :, 0].contiguous(), length, sel[:, :, 0].tolist())
+
+
+def test_attn_bad_ids_and_lengths():
+    c = filled(1, 3, 1, 64, 16, "int8", [64, 40, 64])
+    q = rnd(24, 1, 3, 2, 128)
+    check_attn(c, q, [64, 40, 64], [[[[0, 4, 2]], [[-2, 1, 99]], [[2 ** 31 - 1, -2 ** 31, -1]]]],
+               status=milo.MILO_ERR_BOUNDS)
+    check_attn(c, q, [-1, 40, 65], status=milo.MILO_ERR_BOUNDS)
+    check_attn(c, q, [64, 2 ** 31 - 1, -2 ** 31], status=milo.MILO_ERR_BOUNDS)
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_attn_long_and_ragged(dtype, dt):
+    length = [9000, 3, 4097, 640]
+    c = filled(1, 4, 2, 9000, 64, dtype, length)
+    q = rnd(25, 1, 4, 14, 128, dtype=dt)
+    check_attn(c, q, length)
+    check_attn(c, q, length, scale=0.5)
+    sel = milo.milo_kv_select(c, q, i32(length), 20, 1, 2)
+    check_attn(c, q, length, sel.cpu().tolist())
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("dtype", KINDS)
+def test_attn_large_and_small_values(dtype, dt):
+    """Scores of hundreds, tiny and huge queries, values whose scales span 2^60, rows of zeros."""
+    L, S, H, n = 1, 3, 1, 130
+    c = make(L, S, H, 160, 16, dtype)
+    k, v = rnd(26, L, S, H, n, 128, scale=4.0), rnd(27, L, S, H, n, 128)
+    if dtype != "int4":
+        v *= torch.exp2(torch.randint(-30, 31, (L, S, H, n, 1), generator=torch.Generator().manual_seed(3))).cuda()
+    k[0, 0, 0, 5], v[0, 0, 0, 7], k[0, 1] = 0.0, 0.0, 0.0
+    append(c, k, v, [0] * S)
+    q = rnd(28, L, S, 5, 128, dtype=dt)
+    q[0, 0, 0] *= 100.0
+    q[0, 0, 1] *= 1e-20
+    q[0, 0, 2] = 0.0
+    q[0, 2, 0] *= 1e-3
+    q[0, 2, 1, 1:] *= 1e-6                                       # one loud channel
+    check_attn(c, q, [n, n, 77])
+    check_attn(c, q, [n, n, 77], [[[[0, 3, 8]], [[2, 2, 2]], [[4, 1, 0]]]])
+
+
+def test_attn_query_that_is_not_finite_spoils_its_own_row_alone():
+    c = filled(1, 1, 1, 40, 16, "int8", [40])
+    q = rnd(29, 1, 1, 8, 128)
+    q[0, 0, 3, 5], q[0, 0, 6, 0] = math.nan, math.inf
+    out, lse = milo.milo_kv_attn(c, q, i32([40]), return_lse=True)
+    clean = torch.where(torch.isfinite(q), q, 0.0)
+    ref, rl = milo.milo_kv_attn(c, clean, i32([40]), return_lse=True)
+    good = [0, 1, 2, 4, 5, 7]
+    assert torch.equal(out[:, :, good], ref[:, :, good]) and torch.equal(lse[:, :, good], rl[:, :, good])
+    assert not torch.isfinite(out[0, 0, [3, 6]]).any()
+    ok()
+
+
+def test_attn_same_call_same_bits():
+    length = [9000, 3, 4097, 640]
+    c = filled(1, 4, 2, 9000, 64, "int8", length)
+    q = rnd(30, 1, 4, 14, 128)
+    a = milo.milo_kv_attn(c, q, i32(length))
+    for _ in range(3):
+        assert torch.equal(a, milo.milo_kv_attn(c, q, i32(length)))
+
+
+def test_attn_writes_only_its_output():
+    c = filled(1, 2, 1, 50, 16, "fp8", [50, 0])
+    q = rnd(31, 1, 2, 3, 128, dtype=BF)
+    buf = torch.full((2 * 3 * 128 + 256,), 7.0, dtype=BF, device="cuda")
+    n = milo.milo_kv_attn_workspace_size(c.shape, 1, 3)
+    ws = torch.full((n + 512,), 0xAB, dtype=torch.uint8, device="cuda")
+    keep = c.buf.clone()
+    milo.milo_kv_attn(c, q, i32([50, 0]), out=buf[128:-128].view(1, 2, 3, 128), workspace=ws[:n])
+    ok()
+    assert (buf[:128] == 7).all() and (buf[-128:] == 7).all() and (ws[n:] == 0xAB).all() and torch.equal(c.buf, keep)
+
+
+# ------------------------------------------------- as they are used together
+def test_one_layer_of_a_cache_is_a_cache():
+    L, S, H = 3, 2, 2
+    a, b = make(L, S, H, 50, 16, "int4"), make(L, S, H, 50, 16, "int4")
+    k, v = rnd(32, L, S, H, 50, 128, dtype=BF), rnd(33, L, S, H, 50, 128, dtype=BF)
+    q = rnd(34, L, S, 6, 128, dtype=BF)
+    append(a, k, v, [0, 0])
+    whole = milo.milo_kv_attn(a, q, i32([50, 31]))
+    for l in range(L):
+        append(b.layer(l), k[l:l + 1], v[l:l + 1], [0, 0])
+        assert torch.equal(milo.milo_kv_attn(b.layer(l), q[l:l + 1], i32([50, 31])), whole[l:l + 1])
+    assert torch.equal(a.buf, b.buf)
+
+
+def _steps(c, qkv, start, G, n_steps, stream=None, n_sel=3):
+    """A few decode steps as a model makes them: turn, append, pick blocks, attend."""
+    L, S, H = c.shape.L, c.shape.S, c.shape.H
+    p = milo.rope_params(128, 1e4)
+    length = start.clone()
+    outs = []
+    for t in range(n_steps):
+        x = qkv[t]                                               # [L][S][(G + 2) H][128]
+        n = (G + 1) * H
+        r = milo.milo_rope(x.view(L * S, (G + 2) * H, 128)[:, :n], length, p, stream=stream).view(L, S, n, 128)
+        v = x[:, :, n:].unsqueeze(3)
+        k = r[:, :, G * H:].unsqueeze(3)
+        milo.milo_kv_append(c, k.contiguous(), v.contiguous(), length, stream=stream)
+        length = length + 1
+        q = r[:, :, :G * H].contiguous()
+        sel = milo.milo_kv_select(c, q, length, n_sel, 1, 1, stream=stream)
+        outs.append((milo.milo_kv_attn(c, q, length, sel, stream=stream), q, sel, length))
+    return outs
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+def test_decode_steps(dtype):
+    L, S, H, G, bl = 2, 3, 2, 4, 16
+    c = make(L, S, H, 120, bl, dtype)
+    k, v = rnd(35, L, S, H, 90, 128, dtype=BF), rnd(36, L, S, H, 90, 128, dtype=BF)
+    start = [90, 31, 0]
+    append(c, k, v, [0] * 3, start)
+    qkv = rnd(37, 6, L, S, (G + 2) * H, 128, dtype=BF)
+    for out, q, sel, length in _steps(c, qkv, i32(start), G, 6):
+        assert (length.cpu() <= 120).all()
+    ok()
+    # the last step, whose cache is the one that is held now
+    _, lse = milo.milo_kv_attn(c, q, length, sel, return_lse=True)
+    check_attn(c, q, length.tolist(), sel.cpu().tolist(), out=out, lse=lse)
+
+
+def test_two_streams_and_a_captured_graph():
+    L, S, H, G = 1, 2, 1, 3
+    qkv = rnd(38, 4, L, S, (G + 2) * H, 128, dtype=BF)
+    k = rnd(39, L, S, H, 40, 128, dtype=BF)
+
+    def fresh():
+        c = make(L, S, H, 64, 16, "int8")
+        append(c, k, k, [0, 0], [40, 7])
+        return c
+    want = [o[0] for o in _steps(fresh(), qkv, i32([40, 7]), G, 4)]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    ca, cb = fresh(), fresh()
+    torch.cuda.synchronize()
+    got = {}
+    for s, c in ((a, ca), (b, cb)):
+        with torch.cuda.stream(s):
+            got[s] = [o[0] for o in _steps(c, qkv, i32([40, 7]), G, 4)]
+    torch.cuda.synchronize()
+    for s in (a, b):
+        assert all(torch.equal(x, y) for x, y in zip(got[s], want))
+    # captured once, replayed on other inputs
+    c, start, x = fresh(), i32([40, 7]), torch.zeros_like(qkv)
+    _steps(fresh(), x, start, G, 4)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = [o[0] for o in _steps(c, x, start, G, 4)]
+    x.copy_(qkv)
+    for _ in range(2):
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    ok()
+
+
+# -------------------------------------- with the compressed blocks, one softmax
+def test_decode_over_compressed_blocks_and_cache(oracle_mod):
+    w = synth.WORKLOADS["qwen3b-1layer"]
+    K, V = synth.workload_cache(w)
+    f = milo.milo_compress(K.cuda(), V.cuda(), w.block_len, milo.default_params(factor_dtype="bf16"))
+    q, sel, pos = (t.cuda() for t in synth.decode_inputs(w))
+    S = q.shape[1]
+    plain = milo.milo_decode_attn(f, q, sel, pos, rope_base=w.rope_base)
+    for dtype in KINDS:
+        c = make(w.L, S, w.H, 200, 16, dtype)
+        k, v = rnd(40, w.L, S, w.H, 150, 128), rnd(41, w.L, S, w.H, 150, 128)
+        append(c, k, v, [0] * S)
+        empty = milo.milo_decode_attn_kv(f, q, sel, c, i32([0] * S), positions=pos, rope_base=w.rope_base)
+        assert torch.equal(empty, plain)
+        kt, vt = milo.milo_kv_read(c, i32([0] * S), 150)
+        for n in (1, 150):
+            # the same tokens as a plain fp32 tail: the two tail kernels share the merge, so the difference is
+            # theirs alone, at most that of fp32 attention over 150 tokens of size 1
+            want = milo.milo_decode_attn_tail(f, q, sel, kt, vt, i32([n] * S), pos, rope_base=w.rope_base)
+            got = milo.milo_decode_attn_kv(f, q, sel, c, i32([n] * S), positions=pos, rope_base=w.rope_base)
+            assert float((got - want).abs().max()) <= 2e-5 * float(want.abs().max())
+        ks = torch.tensor([3, 0, -1], dtype=torch.int32).repeat(w.L, S, w.H, 1).cuda()
+        got = milo.milo_decode_attn_kv(f, q, sel, c, i32([150] * S), ks, pos, rope_base=w.rope_base)
+        idx = torch.cat([torch.arange(48, 64), torch.arange(0, 16)]).cuda()
+        want = milo.milo_decode_attn_tail(f, q, sel, kt[:, :, :, idx].contiguous(), vt[:, :, :, idx].contiguous(),
+                                          i32([32] * S), pos, rope_base=w.rope_base)
+        assert float((got - want).abs().max()) <= 2e-5 * float(want.abs().max())
+    ok()
+    L = milo.lib()
+    other = milo.kv_shape(w.L, S + 1, w.H, 200, 16, "int8")
+    big = torch.zeros(milo.milo_kv_cache_size(other), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    args = (f.handle, q.data_ptr(), S, w.Hq, sel.data_ptr(), pos.data_ptr(), sel.shape[1], 1e6, ctypes.byref(other),
+            big.data_ptr(), big.numel(), i32([0] * (S + 1)).data_ptr(), None, 0, plain.data_ptr(), ws.data_ptr())
+    assert L.milo_decode_attn_kv(*args, ws.numel(), None) == milo.MILO_ERR_INVALID_ARG
+    n = L.milo_decode_kv_workspace_size(f.handle, S, w.Hq, sel.shape[1], ctypes.byref(c.shape), 0)
+    args = args[:8] + (ctypes.byref(c.shape), c.buf.data_ptr(), c.buf.numel()) + args[11:]
+    assert L.milo_decode_attn_kv(*args, n - 1, None) == milo.MILO_ERR_WORKSPACE
+
+
+def test_stage_timing_counts_the_calls():
+    c = filled(1, 1, 1, 40, 16, "int8", [40])
+    q = rnd(42, 1, 1, 2, 128)
+    milo.milo_timing_enable()
+    milo.milo_rope(q.view(1, 2, 128), i32([3]), milo.rope_params(128))
+    milo.milo_kv_read(c, i32([0]), 4)
+    append(c, q[:, :, :1, None], q[:, :, :1, None], [3])
+    milo.milo_kv_attn(c, q, i32([40]), milo.milo_kv_select(c, q, i32([40]), 2))
+    t = milo.milo_timing_read()
+    milo.milo_timing_enable(False)
+    for name in ("rope", "kv_write", "kv_read", "kv_select", "kv_attn"):
+        assert t[name][1] == 1 and t[name][0] > 0
