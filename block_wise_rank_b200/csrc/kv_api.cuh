@@ -132,32 +132,85 @@ template <typename T> void kv_read_launch(const KvReadArgs &a, dim3 grid, cudaSt
     else k_kv_read<T, MILO_INT4><<<grid, 256, 0, s>>>(a);
 }
 
-template <typename T> void kv_attn_rows_launch(const KvAttnArgs &a, int64_t rows, cudaStream_t s) {
-    const unsigned grid = (unsigned)((rows + 3) / 4);
-    if (a.c.dtype == MILO_INT8) k_kv_attn_rows<T, MILO_INT8><<<grid, 128, 0, s>>>(a);
-    else if (a.c.dtype == MILO_FP8) k_kv_attn_rows<T, MILO_FP8><<<grid, 128, 0, s>>>(a);
-    else k_kv_attn_rows<T, MILO_INT4><<<grid, 128, 0, s>>>(a);
+// Query rows of a line and the launch shape of an attention call.
+struct KvAttnPlan {
+    int nt, row_tiles, grid;
+    int64_t classes;
+    size_t part_o, part_ml, split, bytes;    // workspace offsets
+};
+
+KvAttnPlan kv_attn_plan(const milo_kv_shape *s, int32_t n_q, int32_t Hq, int32_t n_sel) {
+    KvAttnPlan p{};
+    const int64_t G = Hq / s->H, rows = n_sel ? G : G * n_q;
+    p.nt = rows <= 8 ? 1 : 2;
+    const int rpt = 8 * p.nt;
+    p.row_tiles = (int)((rows + rpt - 1) / rpt);
+    p.classes = (int64_t)s->S * (n_sel ? n_q : 1) * p.row_tiles;
+    // units at most: a CTA with none would have nothing to do
+    const int64_t tiles = n_sel ? (int64_t)n_sel * (s->block_len / 16) : ((int64_t)s->cap + 15) / 16;
+    const int64_t units = p.classes * s->L * s->H * ((tiles + KA_WARPS - 1) / KA_WARPS);
+    p.grid = (int)std::min<int64_t>(units, 2 * sm_count());
+    p.part_o = 0;
+    p.part_ml = align_up(sizeof(float) * 2 * (size_t)p.grid * rpt * D);
+    p.split = p.part_ml + align_up(sizeof(float2) * 2 * (size_t)p.grid * rpt);
+    p.bytes = p.split + align_up(sizeof(longlong2) * (size_t)p.grid);
+    return p;
+}
+
+// opt-in shared memory of a kernel, once per device
+template <typename K> cudaError_t kv_smem(K kernel, size_t bytes, bool (&done)[64]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) done[dev] = true;
+    return e;
+}
+
+template <typename T, int DT, int NT, bool SEL> cudaError_t kv_attn_run(const KvAttnArgs &a, int grid, cudaStream_t s) {
+    static bool done[64];
+    const size_t smem = sizeof(KaSmem<T, NT>);
+    const cudaError_t e = kv_smem(k_kv_attn<T, DT, NT, SEL>, smem, done);
+    if (e != cudaSuccess) return e;
+    k_kv_attn<T, DT, NT, SEL><<<grid, KA_THREADS, smem, s>>>(a);
+    if (grid > 1) k_kv_attn_merge<T, NT, SEL><<<dim3(grid, 8 * NT), 32 * KA_MERGE_WARPS, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, int DT> cudaError_t kv_attn_rows(const KvAttnArgs &a, int nt, int grid, cudaStream_t s) {
+    if (a.sel) return nt == 1 ? kv_attn_run<T, DT, 1, true>(a, grid, s) : kv_attn_run<T, DT, 2, true>(a, grid, s);
+    return nt == 1 ? kv_attn_run<T, DT, 1, false>(a, grid, s) : kv_attn_run<T, DT, 2, false>(a, grid, s);
+}
+
+template <typename T> cudaError_t kv_attn_type(const KvAttnArgs &a, int nt, int grid, cudaStream_t s) {
+    if (a.c.dtype == MILO_INT8) return kv_attn_rows<T, MILO_INT8>(a, nt, grid, s);
+    if (a.c.dtype == MILO_FP8) return kv_attn_rows<T, MILO_FP8>(a, nt, grid, s);
+    return kv_attn_rows<T, MILO_INT4>(a, nt, grid, s);
 }
 
 milo_status kv_attn_launch(const milo_kv_shape *shape, const void *cache, const void *q, milo_dtype q_dtype,
                            int32_t n_q, int32_t Hq, const int32_t *len, const int32_t *selected, int32_t n_sel,
                            double scale, void *out, float *lse, float2 *ml, void *workspace, cudaStream_t s) {
-    (void)workspace;
+    const KvAttnPlan p = kv_attn_plan(shape, n_q, Hq, n_sel);
     KvAttnArgs a{};
     a.c = kv_view(shape, cache);
     a.q = q; a.out = out; a.lse = lse; a.ml = ml; a.len = len; a.sel = selected;
     a.n_q = n_q; a.G = Hq / shape->H; a.n_sel = n_sel;
-    a.scale = scale > 0.0 ? (float)scale : (float)(1.0 / std::sqrt((double)D));
-    const int64_t rows = (int64_t)shape->L * shape->S * n_q * Hq;
-    if (q_dtype == MILO_BF16) kv_attn_rows_launch<__nv_bfloat16>(a, rows, s);
-    else kv_attn_rows_launch<float>(a, rows, s);
-    return cuda_check(cudaGetLastError(), "kv attention launch");
+    a.tpb = shape->block_len / 16;
+    a.tpb_magic = a.tpb == 1 ? 0u : (uint32_t)(((1ull << 32) + a.tpb - 1) / a.tpb);
+    a.row_tiles = p.row_tiles; a.classes = p.classes;
+    a.scale = (float)((scale > 0.0 ? scale : 1.0 / std::sqrt((double)D)) * 1.4426950408889634074);
+    a.part_o = (float *)((char *)workspace + p.part_o);
+    a.part_ml = (float2 *)((char *)workspace + p.part_ml);
+    a.split = (longlong2 *)((char *)workspace + p.split);
+    return cuda_check(q_dtype == MILO_BF16 ? kv_attn_type<__nv_bfloat16>(a, p.nt, p.grid, s)
+                                           : kv_attn_type<float>(a, p.nt, p.grid, s), "kv attention launch");
 }
 
-// selection of a call: NULL and 0, or ids and 1 .. n_b of them
+// selection of a call: NULL and 0, or ids and how many (their tokens at most 2^30)
 bool kv_selection_ok(const milo_kv_shape *s, const int32_t *selected, int32_t n_sel) {
     if (!selected) return n_sel == 0;
-    return aligned(selected, 4) && n_sel >= 1;
+    return aligned(selected, 4) && n_sel >= 1 && (int64_t)n_sel * s->block_len <= (int64_t(1) << 30);
 }
 
 }  // namespace
@@ -352,7 +405,7 @@ milo_status milo_kv_select(const milo_kv_shape *shape, const void *cache, size_t
 
 size_t milo_kv_attn_workspace_size(const milo_kv_shape *shape, int32_t n_q, int32_t Hq, int32_t n_sel) {
     if (!kv_ok(shape) || shape->d != D || n_q <= 0 || Hq <= 0 || Hq % shape->H || n_sel < 0) return 0;
-    return kAlign;
+    return kv_attn_plan(shape, n_q, Hq, n_sel).bytes;
 }
 
 milo_status milo_kv_attn(const milo_kv_shape *shape, const void *cache, size_t cache_bytes, const void *q,

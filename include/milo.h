@@ -543,7 +543,8 @@ size_t milo_kv_attn_workspace_size(const milo_kv_shape *shape, int32_t n_q, int3
  *   len:      as milo_kv_select
  *   selected: device, int32 [L][S][n_q][H][n_sel] block ids (as milo_kv_select
  *             writes them; any order), -1 = none, or NULL for all tokens (n_sel =
- *             0).  An id listed twice counts twice; another id outside [0, n_b)
+ *             0; n_sel * block_len at most 2^30).  An id listed twice counts
+ *             twice; another id outside [0, n_b)
  *             sets MILO_ERR_BOUNDS and contributes nothing.
  *   scale:    > 0, or 0 for 1 / sqrt(d)
  *   lse:      device, float [L][S][n_q][Hq] out: the logarithm of the sum of
