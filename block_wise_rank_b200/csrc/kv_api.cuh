@@ -134,8 +134,7 @@ template <typename T> void kv_read_launch(const KvReadArgs &a, dim3 grid, cudaSt
 
 // Query rows of a line and the launch shape of an attention call.
 struct KvAttnPlan {
-    int nt, row_tiles, grid;
-    int64_t classes;
+    int nt, row_tiles, grid, classes;
     size_t part_o, part_ml, split, bytes;    // workspace offsets
 };
 
@@ -145,15 +144,18 @@ KvAttnPlan kv_attn_plan(const milo_kv_shape *s, int32_t n_q, int32_t Hq, int32_t
     p.nt = rows <= 8 ? 1 : 2;
     const int rpt = 8 * p.nt;
     p.row_tiles = (int)((rows + rpt - 1) / rpt);
-    p.classes = (int64_t)s->S * (n_sel ? n_q : 1) * p.row_tiles;
+    p.classes = (int)((int64_t)s->S * (n_sel ? n_q : 1) * p.row_tiles);   // at most the query rows
     // units at most: a CTA with none would have nothing to do
+    const int warps = p.nt == 1 ? KaShape<1>::WARPS : KaShape<2>::WARPS;
+    const int begin = p.nt == 1 ? KaShape<1>::BEGIN : KaShape<2>::BEGIN;
+    const int ctas = p.nt == 1 ? KaShape<1>::CTAS : KaShape<2>::CTAS;
     const int64_t tiles = n_sel ? (int64_t)n_sel * (s->block_len / 16) : ((int64_t)s->cap + 15) / 16;
-    const int64_t units = p.classes * s->L * s->H * ((tiles + KA_WARPS - 1) / KA_WARPS);
-    p.grid = (int)std::min<int64_t>(units, 2 * sm_count());
+    const int64_t units = (int64_t)p.classes * s->L * s->H * (begin + (tiles + warps - 1) / warps);
+    p.grid = (int)std::min<int64_t>(units, ctas * sm_count());
     p.part_o = 0;
     p.part_ml = align_up(sizeof(float) * 2 * (size_t)p.grid * rpt * D);
     p.split = p.part_ml + align_up(sizeof(float2) * 2 * (size_t)p.grid * rpt);
-    p.bytes = p.split + align_up(sizeof(longlong2) * (size_t)p.grid);
+    p.bytes = p.split + align_up(sizeof(int4) * (size_t)p.grid);
     return p;
 }
 
@@ -169,11 +171,14 @@ template <typename K> cudaError_t kv_smem(K kernel, size_t bytes, bool (&done)[6
 
 template <typename T, int DT, int NT, bool SEL> cudaError_t kv_attn_run(const KvAttnArgs &a, int grid, cudaStream_t s) {
     static bool done[64];
-    const size_t smem = sizeof(KaSmem<T, NT>);
+    const size_t smem = sizeof(KaSmem<T, DT, NT>);
     const cudaError_t e = kv_smem(k_kv_attn<T, DT, NT, SEL>, smem, done);
     if (e != cudaSuccess) return e;
-    k_kv_attn<T, DT, NT, SEL><<<grid, KA_THREADS, smem, s>>>(a);
-    if (grid > 1) k_kv_attn_merge<T, NT, SEL><<<dim3(grid, 8 * NT), 32 * KA_MERGE_WARPS, 0, s>>>(a);
+    k_kv_attn<T, DT, NT, SEL><<<grid, 32 * KaShape<NT>::WARPS, smem, s>>>(a);
+    // many parts a line: a CTA per row, else one for the line
+    const int64_t lines = (int64_t)a.classes * a.c.L * a.c.H;
+    if (grid > 1)
+        k_kv_attn_merge<T, NT, SEL><<<dim3(grid, grid >= 16 * lines ? 8 * NT : 1), 32 * KA_MERGE_WARPS, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -202,7 +207,7 @@ milo_status kv_attn_launch(const milo_kv_shape *shape, const void *cache, const 
     a.scale = (float)((scale > 0.0 ? scale : 1.0 / std::sqrt((double)D)) * 1.4426950408889634074);
     a.part_o = (float *)((char *)workspace + p.part_o);
     a.part_ml = (float2 *)((char *)workspace + p.part_ml);
-    a.split = (longlong2 *)((char *)workspace + p.split);
+    a.split = (int4 *)((char *)workspace + p.split);
     return cuda_check(q_dtype == MILO_BF16 ? kv_attn_type<__nv_bfloat16>(a, p.nt, p.grid, s)
                                            : kv_attn_type<float>(a, p.nt, p.grid, s), "kv attention launch");
 }

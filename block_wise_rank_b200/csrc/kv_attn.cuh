@@ -7,13 +7,13 @@
 // byte and query head), so memory bounds it as long as the codes reach the
 // tensor cores cheaply:
 //
-// * A warp takes 16 tokens at a time straight from memory into the operand
-//   registers of m16n8k16: tokens are the rows of the score product (A = K, B =
-//   up to 8 NT queries from shared memory), channels those of the value
-//   product (A = V^T, B = the weights, transposed between the two by movmatrix).
-//   Both products sum over an index whose order is free, so a thread's 16-byte
-//   loads are already fragments; codes become fp16 exactly (INT8 and e4m3 times
-//   the row's scale later, INT4 as the fp16 value it stands for).
+// * A warp takes 16 tokens at a time from its own ring of asynchronous copies: tokens
+//   are the rows of the score product (m16n8k16, A = K, B = up to 8 NT queries),
+//   channels those of the value product (A = V^T, B = the weights, transposed
+//   between the two by movmatrix).  Both products sum over an index whose order
+//   is free, so a thread's 16-byte reads are already fragments; codes become
+//   fp16 exactly (INT8 and e4m3 times the row's scale later, INT4 as the fp16
+//   value it stands for).
 // * Row scales never touch the rows: the key's multiplies the score, the
 //   value's the weight.  A weight is kept as p * v_scale / 2^E * 2^10 in fp16,
 //   with E the greatest exponent of the scales so far.
@@ -46,14 +46,18 @@ struct KvAttnArgs {
     int tpb;                       // tiles of 16 tokens per block
     uint32_t tpb_magic;            // ceil(2^32 / tpb), 0 for tpb = 1
     int row_tiles;                 // query tiles of a line's rows
-    int64_t classes;               // S * row_tiles (dense), S * n_q * row_tiles (selected)
+    int classes;                   // S * row_tiles (dense), S * n_q * row_tiles (selected)
     float scale;                   // softmax scale * log2(e)
     float *part_o;                 // [2 grid][8 NT][D] normalised outputs of parts
     float2 *part_ml;               // [2 grid][8 NT] (reference, sum) of parts, in powers of two
-    longlong2 *split;              // [grid] line that a CTA begins and others end, or -1; its last CTA
+    int4 *split;                   // [grid] (class, layer, head, last CTA) of a line that a CTA begins and others end; -1: none
 };
 
-constexpr int KA_WARPS = 8, KA_THREADS = 32 * KA_WARPS, KA_UNIT = 16 * KA_WARPS;
+// CTA shape by the query tiles of a warp: 8 NT rows
+template <int NT> struct KaShape {
+    static constexpr int WARPS = NT == 1 ? 8 : 4, CTAS = NT == 1 ? 2 : 3;   // warps of a CTA, CTAs of an SM
+    static constexpr int BEGIN = NT == 1 ? 1 : 2;   // units that beginning and ending a line costs, counted at its front
+};
 constexpr float KA_RAISE = 4.f;        // a score this far above the reference raises it
 constexpr float KA_SHIFT = 10.f;       // weights are kept times 2^10 (fp16's subnormals begin at 2^-14)
 
@@ -76,17 +80,6 @@ __device__ __forceinline__ float ka_exp2(float x) {
 }
 __device__ __forceinline__ uint32_t ka_u(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 __device__ __forceinline__ __half2 ka_h(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
-__device__ __forceinline__ uint4 ka_ldg16(const unsigned char *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint2 ka_ldg8(const unsigned char *p) {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
-}
 
 // INT8: bytes (biased by 128) b0, b1 (sel 0x4140) or b2, b3 (0x4342) of x under
 // the high byte of 1024 + code + 128
@@ -111,120 +104,152 @@ template <bool HI> __device__ __forceinline__ uint32_t ka_int4(uint32_t x, __hal
 }
 
 // ---------------------------------------------------------- a tile's codes
-// Keys: rows t0 + g and t0 + g + 8, values: rows t0 + {2c, 2c + 1, 2c + 8, 2c + 9}
-// (g = lane / 4, c = lane % 4).  Rows from `end` on are neither read nor used.
-template <int DT> struct KaTile;
-
-template <> struct KaTile<MILO_INT8> {
-    uint4 k[4], v[4];
-    float ks[2], vs[2];
-};
-template <> struct KaTile<MILO_FP8> : KaTile<MILO_INT8> {};
-template <> struct KaTile<MILO_INT4> {
-    uint4 k[2];
-    uint2 v[4];
-    uint32_t kp[2], vp[4];       // (scale, zero) of the thread's group in each row
+// A warp's ring in shared memory holds a tile of 16 tokens per stage: keys,
+// values, then the parameters, brought by 16-byte asynchronous copies (rows from
+// `end` on are filled with zeros and not read; t0 is a row of the line).  Row r of the score product is
+// token ka_token(r) of the tile, and so is index r of the value product; that
+// and the exchange of 16-byte chunks below let the fragments' reads touch every bank
+// once.
+template <int DT> struct KaTile {
+    static constexpr int ROW = DT == MILO_INT4 ? D / 2 : D;
+    static constexpr int PAR = DT == MILO_INT4 ? 4 * KV_NG : 4;
+    static constexpr int V = 16 * ROW, KP = 32 * ROW, VP = KP + 16 * PAR, BYTES = KP + 32 * PAR;
+    static constexpr int STAGES = DT == MILO_INT4 ? 5 : 3;
 };
 
 template <int DT> struct KaLine {
     const unsigned char *k, *v, *kp, *vp;
 };
 
-template <int DT>
-__device__ __forceinline__ void ka_load_k(KaTile<DT> &t, const KaLine<DT> &ln, int64_t t0, int64_t end, int g, int c) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int64_t row = t0 + g + 8 * r;
-        const bool ok = row < end;
-        if constexpr (DT == MILO_INT4) {
-            t.k[r] = make_uint4(0u, 0u, 0u, 0u);
-            t.kp[r] = 0u;
-            if (ok) {
-                t.k[r] = ka_ldg16(ln.k + row * 64 + 16 * c);
-                t.kp[r] = __ldg(reinterpret_cast<const uint32_t *>(ln.kp + row * 16) + c);
-            }
-        } else {
-            t.k[2 * r] = t.k[2 * r + 1] = make_uint4(0u, 0u, 0u, 0u);
-            t.ks[r] = t.vs[r] = 0.f;
-            if (ok) {
-                t.k[2 * r] = ka_ldg16(ln.k + row * 128 + 16 * c);
-                t.k[2 * r + 1] = ka_ldg16(ln.k + row * 128 + 64 + 16 * c);
-                t.ks[r] = __ldg(reinterpret_cast<const float *>(ln.kp) + row);
-                t.vs[r] = __ldg(reinterpret_cast<const float *>(ln.vp) + row);
-            }
-        }
-    }
+template <int DT> __device__ __forceinline__ int ka_token(int r) { return DT == MILO_INT4 ? r ^ ((r >> 1) & 1) : r; }
+// where 16-byte chunk `c` of row `t` lies in its row
+template <int DT> __device__ __forceinline__ int ka_chunk(int t, int c) {
+    return DT == MILO_INT4 ? c ^ ((t >> 1) & 2) : c ^ ((t & 6) ^ ((t & 1) << 2));
 }
 
+__device__ __forceinline__ void ka_copy16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ka_copy4(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void ka_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void ka_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// rows t0 .. t0 + 15 of a line into the stage at shared address `dst`
 template <int DT>
-__device__ __forceinline__ void ka_load_v(KaTile<DT> &t, const KaLine<DT> &ln, int64_t t0, int64_t end, int g, int c) {
+__device__ __forceinline__ void ka_fetch(uint32_t dst, const KaLine<DT> &ln, int t0, int end, int lane) {
+    using Tl = KaTile<DT>;
+    constexpr int PER = Tl::ROW / 16, STEP = 32 / PER;       // chunks of a row, rows per round of the warp
+    const int c = lane % PER, r0 = lane / PER, rem = end - t0;
+    const int64_t at = (int64_t)t0 * Tl::ROW + (r0 * Tl::ROW + 16 * c);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int64_t row = t0 + 2 * c + (r & 1) + 8 * (r >> 1);
-        const bool ok = row < end;
-        if constexpr (DT == MILO_INT4) {
-            t.v[r] = make_uint2(0u, 0u);
-            t.vp[r] = 0u;
-            if (ok) {
-                t.v[r] = ka_ldg8(ln.v + row * 64 + 8 * g);
-                t.vp[r] = __ldg(reinterpret_cast<const uint32_t *>(ln.vp + row * 16) + g / 2);
-            }
-        } else {
-            t.v[r] = make_uint4(0u, 0u, 0u, 0u);
-            if (ok) t.v[r] = ka_ldg16(ln.v + row * 128 + 16 * g);
-        }
+    for (int i = 0; i < 16 / STEP; ++i) {
+        const int r = r0 + STEP * i;
+        const uint32_t to = dst + r * Tl::ROW + 16 * ka_chunk<DT>(r, c);
+        ka_copy16(to, ln.k + at + STEP * i * Tl::ROW, r < rem);
+        ka_copy16(to + Tl::V, ln.v + at + STEP * i * Tl::ROW, r < rem);
+    }
+    const int r = lane & 15;
+    const unsigned char *p = (lane < 16 ? ln.kp : ln.vp) + ((int64_t)t0 * Tl::PAR + r * Tl::PAR);
+    const uint32_t to = dst + (lane < 16 ? Tl::KP : Tl::VP) + r * Tl::PAR;
+    if (DT == MILO_INT4) ka_copy16(to, p, r < rem);
+    else ka_copy4(to, p, r < rem);
+}
+
+// channel of element e (0..3: b0 low, b0 high, b1 low, b1 high) of the queries'
+// fragment for step j of the score product, thread column c, and its inverse:
+// the order in which the keys' codes come
+//   8 bits: (j < 4 ? 16 c + 4 j : 64 + 16 c + 4 (j - 4)) + e
+//   4 bits: 32 c + 8 (j / 2) + 2 (j % 2) + e / 2 + 4 (e % 2)
+template <int DT> __device__ __forceinline__ void ka_place(int ch, int &j, int &c, int &e) {
+    if (DT == MILO_INT4) {
+        c = ch / 32;
+        j = 2 * ((ch % 32) / 8) + (ch % 4) / 2;
+        e = 2 * (ch % 2) + (ch % 8) / 4;
+    } else {
+        c = (ch % 64) / 16;
+        j = (ch / 64) * 4 + (ch % 16) / 4;
+        e = ch % 4;
     }
 }
 
 __device__ __forceinline__ uint32_t ka_word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// channel of element e (0..3: b0 low, b0 high, b1 low, b1 high) of the queries'
-// fragment for step j of the score product, thread column c: the order in which
-// the keys' codes come
-template <int DT> __device__ __forceinline__ int ka_channel(int j, int c, int e) {
-    if (DT == MILO_INT4) return 32 * c + 8 * (j / 2) + 2 * (j % 2) + (e / 2) + 4 * (e % 2);
-    return (j < 4 ? 16 * c + 4 * j : 64 + 16 * c + 4 * (j - 4)) + e;
-}
-
-// A fragment of step j of the score product
-template <int DT> __device__ __forceinline__ void ka_frag_k(const KaTile<DT> &t, int j, uint32_t (&a)[4]) {
+// The A fragments of four steps of the score product (half 0: steps 0-3, half 1: 4-7)
+template <int DT> __device__ __forceinline__ void ka_frag_k(const unsigned char *st, int half, int g, int c, uint32_t (&a)[4][4]) {
+    using Tl = KaTile<DT>;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
+        const int t = ka_token<DT>(g + 8 * r);
         if constexpr (DT == MILO_INT4) {
-            const __half2 s = ka_h(__byte_perm(t.kp[r], 0u, 0x1010)), z = ka_h(__byte_perm(t.kp[r], 0u, 0x3232));
-            const uint32_t w = ka_word(t.k[r], j / 2) >> (j % 2 ? 8 : 0);
-            a[r] = ka_int4<false>(w, s, z);
-            a[2 + r] = ka_int4<true>(w, s, z);
-        } else {
-            uint32_t w = ka_word(t.k[2 * r + j / 4], j % 4);
-            if constexpr (DT == MILO_INT8) {
-                w ^= 0x80808080u;
-                a[r] = ka_int8(w, 0x4140);
-                a[2 + r] = ka_int8(w, 0x4342);
-            } else {
-                a[r] = ka_fp8(w, 0x1404);
-                a[2 + r] = ka_fp8(w, 0x3424);
+            const uint2 w = *reinterpret_cast<const uint2 *>(st + t * Tl::ROW + 16 * ka_chunk<DT>(t, c) + 8 * half);
+            const uint32_t p = *reinterpret_cast<const uint32_t *>(st + Tl::KP + t * Tl::PAR + 4 * c);   // (scale, zero)
+            const __half2 s = ka_h(__byte_perm(p, 0u, 0x1010)), z = ka_h(__byte_perm(p, 0u, 0x3232));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t x = (j < 2 ? w.x : w.y) >> (j % 2 ? 8 : 0);
+                a[j][r] = ka_int4<false>(x, s, z);
+                a[j][2 + r] = ka_int4<true>(x, s, z);
             }
+        } else {
+            const uint4 w = *reinterpret_cast<const uint4 *>(st + t * Tl::ROW + 16 * ka_chunk<DT>(t, c + 4 * half));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t x = ka_word(w, j);
+                if constexpr (DT == MILO_INT8) {
+                    x ^= 0x80808080u;
+                    a[j][r] = ka_int8(x, 0x4140);
+                    a[j][2 + r] = ka_int8(x, 0x4342);
+                } else {
+                    a[j][r] = ka_fp8(x, 0x1404);
+                    a[j][2 + r] = ka_fp8(x, 0x3424);
+                }
+            }
+        }
+    }
+}
+
+// What a thread reads of the tile's values: channels 16 g .. + 15 of tokens
+// r = 2c, 2c + 1, 2c + 8, 2c + 9, 4-bit codes with their (scale, zero)
+template <int DT> struct KaValues {
+    uint4 w[4];
+};
+template <> struct KaValues<MILO_INT4> {
+    uint2 w[4];
+    uint32_t p[4];
+};
+template <int DT> __device__ __forceinline__ void ka_read_v(const unsigned char *st, int g, int c, KaValues<DT> &v) {
+    using Tl = KaTile<DT>;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = ka_token<DT>(2 * c + (i & 1) + 8 * (i >> 1));
+        const unsigned char *row = st + Tl::V + t * Tl::ROW;
+        if constexpr (DT == MILO_INT4) {
+            v.w[i] = *reinterpret_cast<const uint2 *>(row + 16 * ka_chunk<DT>(t, g / 2) + 8 * (g % 2));
+            v.p[i] = *reinterpret_cast<const uint32_t *>(st + Tl::VP + t * Tl::PAR + 4 * (g / 2));
+        } else {
+            v.w[i] = *reinterpret_cast<const uint4 *>(row + 16 * ka_chunk<DT>(t, g));
         }
     }
 }
 
 // A fragments of row tiles 2 w and 2 w + 1 of the value product: channels 16 g +
 // 4 w .. + 3, tokens 2c, 2c + 1 (h = 0) and 2c + 8, 2c + 9 (h = 1)
-template <int DT> __device__ __forceinline__ void ka_frag_v(const KaTile<DT> &t, int w, uint32_t (&a)[2][4]) {
+template <int DT> __device__ __forceinline__ void ka_frag_v(const KaValues<DT> &t, int w, uint32_t (&a)[2][4]) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         if constexpr (DT == MILO_INT4) {
-            const __half2 s = ka_h(__byte_perm(t.vp[2 * h], t.vp[2 * h + 1], 0x5410));
-            const __half2 z = ka_h(__byte_perm(t.vp[2 * h], t.vp[2 * h + 1], 0x7632));
-            const uint32_t A = w < 2 ? t.v[2 * h].x : t.v[2 * h].y, B = w < 2 ? t.v[2 * h + 1].x : t.v[2 * h + 1].y;
+            const __half2 s = ka_h(__byte_perm(t.p[2 * h], t.p[2 * h + 1], 0x5410));
+            const __half2 z = ka_h(__byte_perm(t.p[2 * h], t.p[2 * h + 1], 0x7632));
+            const uint32_t A = w < 2 ? t.w[2 * h].x : t.w[2 * h].y, B = w < 2 ? t.w[2 * h + 1].x : t.w[2 * h + 1].y;
             const uint32_t x = __byte_perm(A, B, w % 2 ? 0x7632 : 0x5410), y = x >> 8;
             a[0][2 * h] = ka_int4<false>(x, s, z);
             a[0][2 * h + 1] = ka_int4<true>(x, s, z);
             a[1][2 * h] = ka_int4<false>(y, s, z);
             a[1][2 * h + 1] = ka_int4<true>(y, s, z);
         } else {
-            const uint32_t A = ka_word(t.v[2 * h], w), B = ka_word(t.v[2 * h + 1], w);
+            const uint32_t A = ka_word(t.w[2 * h], w), B = ka_word(t.w[2 * h + 1], w);
             uint32_t x = __byte_perm(A, B, 0x5140), y = __byte_perm(A, B, 0x7362);   // (A0 B0 A1 B1), (A2 B2 A3 B3)
             if constexpr (DT == MILO_INT8) {
                 x ^= 0x80808080u;
@@ -246,55 +271,83 @@ template <int DT> __device__ __forceinline__ void ka_frag_v(const KaTile<DT> &t,
 // ------------------------------------------------------------------- lines
 // A class is a (session, query, query tile) -- dense: all queries share their
 // lines -- and holds L * H lines of equal length.
-template <bool SEL> struct KaClass {
+template <bool SEL, int NT> struct KaClass {
+    static constexpr int rpt = 8 * NT, KA_WARPS = KaShape<NT>::WARPS;
     int s, i, rt, rows, end;       // rows of the class's query tile, tokens that its last row sees
+    int held;                      // tokens of the session
 
-    __device__ __forceinline__ void set(const KvAttnArgs &a, int64_t k, int rpt, bool tell) {
-        rt = (int)(k % a.row_tiles);
+    __device__ __forceinline__ void set(const KvAttnArgs &a, int k, bool tell) {
+        rt = k % a.row_tiles;
         k /= a.row_tiles;
-        i = SEL ? (int)(k % a.n_q) : 0;
-        s = (int)(SEL ? k / a.n_q : k);
+        i = SEL ? k % a.n_q : 0;
+        s = SEL ? k / a.n_q : k;
+        fill(a, tell);
+    }
+    __device__ __forceinline__ void fill(const KvAttnArgs &a, bool tell) {
         const int all = SEL ? a.G : a.n_q * a.G;
         rows = min(rpt, all - rt * rpt);
-        end = kv_seen(a.len, s, a.n_q, SEL ? i : (rt * rpt + rows - 1) / a.G, a.c.cap, tell);
+        held = kv_seen(a.len, s, 1, 0, a.c.cap, tell);
+        end = seen(a, rows - 1);
     }
-    // 16-token tiles of a line (selected: of all listed blocks)
-    __device__ __forceinline__ int64_t tiles(const KvAttnArgs &a) const {
-        return SEL ? (int64_t)a.n_sel * a.tpb : ((int64_t)end + 15) / 16;
+    __device__ __forceinline__ void next(const KvAttnArgs &a, bool tell) {
+        if (++rt == a.row_tiles) {
+            rt = 0;
+            if (!SEL || ++i == a.n_q) {
+                i = 0;
+                ++s;
+            }
+        }
+        fill(a, tell);
     }
-    __device__ __forceinline__ int64_t units(const KvAttnArgs &a) const {
-        const int64_t u = (tiles(a) + KA_WARPS - 1) / KA_WARPS;
-        return u > 0 ? u : 1;      // an empty line still writes its zeros
+    // 16-token tiles of a line (selected: of all listed blocks); at most 2^26
+    __device__ __forceinline__ int tiles(const KvAttnArgs &a) const {
+        return SEL ? a.n_sel * a.tpb : (end + 15) / 16;
+    }
+    __device__ __forceinline__ int units(const KvAttnArgs &a) const {
+        return KaShape<NT>::BEGIN + (tiles(a) + KA_WARPS - 1) / KA_WARPS;
+    }
+    // tokens that row r sees
+    __device__ __forceinline__ int seen(const KvAttnArgs &a, int r) const {
+        return max(0, held - a.n_q + query(a, r) + 1);
     }
     // query of row r, and the row's index in [L][S][n_q][Hq]
-    __device__ __forceinline__ int query(const KvAttnArgs &a, int r, int rpt) const {
+    __device__ __forceinline__ int query(const KvAttnArgs &a, int r) const {
         return SEL ? i : (rt * rpt + r) / a.G;
     }
-    __device__ __forceinline__ int64_t row(const KvAttnArgs &a, int l, int h, int r, int rpt) const {
+    __device__ __forceinline__ int64_t row(const KvAttnArgs &a, int l, int h, int r) const {
         const int at = rt * rpt + r, g = SEL ? at : at % a.G;
-        return (((int64_t)l * a.c.S + s) * a.n_q + query(a, r, rpt)) * a.c.H * a.G + (int64_t)h * a.G + g;
+        return (((int64_t)l * a.c.S + s) * a.n_q + query(a, r)) * a.c.H * a.G + (int64_t)h * a.G + g;
     }
 };
 
-template <typename T, int NT> struct KaSmem {
+template <typename T, int DT, int NT> struct KaSmem {
     static constexpr int RPT = 8 * NT;                       // query rows of a line
+    static constexpr int KA_WARPS = KaShape<NT>::WARPS;
     static constexpr int PARTS = sizeof(T) == 4 ? 2 : 1;     // fp16 parts of a query
+    static constexpr int RING = KaTile<DT>::STAGES * KaTile<DT>::BYTES, OUT = RPT * (D + 4) * 4;
+    unsigned char ring[KA_WARPS][RING > OUT ? RING : OUT];   // a warp's stages; behind its tiles its output [RPT][D + 4]
     uint32_t q[NT][8][32][2 * PARTS];                        // fragments of the queries, [tile][step][lane]
-    float o[KA_WARPS][RPT][D + 4];                           // the warps' outputs (channel rows padded)
     float m[KA_WARPS][RPT], l[KA_WARPS][RPT];
-    float e[KA_WARPS];                                       // exponent of the warp's value scales
+    float e[KA_WARPS + 1];                                   // 2^E of the warps' value scales, and of the join
     float sc[RPT];                                           // factor on a row's scores
     int seen[RPT];
     int64_t scan[KA_WARPS + 1];
-    int64_t cls, off;
+    int cls;
+    int64_t off;
 };
 
-// out / lse / (max, sum) of one finished row: normalised o, reference m and sum l in powers of two
+// Channels 4 lane .. of one finished row: normalised output; lane 0 adds lse / (max, sum) from the
+// reference m and the sum l in powers of two
 template <typename T>
-__device__ __forceinline__ void ka_finish(const KvAttnArgs &a, int64_t row, int ch, float o, float m, float l) {
-    if constexpr (sizeof(T) == 4) ((float *)a.out)[row * D + ch] = o;
-    else ((__nv_bfloat16 *)a.out)[row * D + ch] = __float2bfloat16_rn(o);
-    if (ch == 0) {
+__device__ __forceinline__ void ka_finish(const KvAttnArgs &a, int64_t row, int lane, float4 o, float m, float l) {
+    if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<float4 *>(a.out)[row * (D / 4) + lane] = o;
+    } else {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(o.x, o.y), y = __floats2bfloat162_rn(o.z, o.w);
+        reinterpret_cast<uint2 *>(a.out)[row * (D / 4) + lane] =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+    }
+    if (lane == 0) {
         const float ln2 = 0.693147180559945309f;
         if (a.lse) a.lse[row] = l != 0.f ? (m + log2f(l)) * ln2 : -INFINITY;
         if (a.ml) a.ml[row] = l != 0.f ? make_float2(m * ln2, l) : make_float2(-INFINITY, 0.f);
@@ -302,28 +355,30 @@ __device__ __forceinline__ void ka_finish(const KvAttnArgs &a, int64_t row, int 
 }
 
 template <typename T, int DT, int NT, bool SEL>
-__global__ void __launch_bounds__(KA_THREADS, 2) k_kv_attn(const __grid_constant__ KvAttnArgs a) {
-    using Sm = KaSmem<T, NT>;
-    constexpr int RPT = Sm::RPT, PARTS = Sm::PARTS;
+__global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_kv_attn(const __grid_constant__ KvAttnArgs a) {
+    using Sm = KaSmem<T, DT, NT>;
+    using Tl = KaTile<DT>;
+    constexpr int RPT = Sm::RPT, PARTS = Sm::PARTS, KA_WARPS = Sm::KA_WARPS, KA_THREADS = 32 * KA_WARPS;
+    constexpr int KA_BEGIN = KaShape<NT>::BEGIN;
     constexpr bool PAR = DT != MILO_INT4;                    // a scale per row
     extern __shared__ __align__(16) unsigned char ka_raw[];
     Sm &sm = *reinterpret_cast<Sm *>(ka_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-    const int64_t LH = (int64_t)a.c.L * a.c.H;
+    const int LH = a.c.L * a.c.H;
 
     // this CTA's run of units [u0, u1) and the class that u0 falls into
     int64_t total;
-    KaClass<SEL> cl;
+    KaClass<SEL, NT> cl;
     if (SEL) {
-        cl.set(a, 0, RPT, false);
-        total = a.classes * LH * cl.units(a);
+        cl.set(a, 0, false);
+        total = (int64_t)a.classes * LH * cl.units(a);
     } else {
-        const int64_t per = (a.classes + KA_THREADS - 1) / KA_THREADS;
-        const int64_t k0 = min(a.classes, tid * per), k1 = min(a.classes, k0 + per);
+        const int per = (a.classes + KA_THREADS - 1) / KA_THREADS;
+        const int k0 = (int)min((int64_t)a.classes, (int64_t)tid * per), k1 = min(a.classes - k0, per) + k0;
         int64_t mine = 0;
-        for (int64_t k = k0; k < k1; ++k) {
-            cl.set(a, k, RPT, blockIdx.x == 0);   // each class once
-            mine += cl.units(a) * LH;
+        for (int k = k0; k < k1; ++k) {
+            cl.set(a, k, blockIdx.x == 0);   // each class once
+            mine += (int64_t)cl.units(a) * LH;
         }
         int64_t inc = mine;
         for (int o = 1; o < 32; o <<= 1) {
@@ -341,10 +396,10 @@ __global__ void __launch_bounds__(KA_THREADS, 2) k_kv_attn(const __grid_constant
         int64_t at = before + inc - mine;                    // first unit of class k0
         const int64_t n = (total + gridDim.x - 1) / gridDim.x, u = blockIdx.x * n;
         if (u >= at && u < at + mine) {
-            int64_t k = k0;
+            int k = k0;
             for (;; ++k) {
-                cl.set(a, k, RPT, false);
-                const int64_t w = cl.units(a) * LH;
+                cl.set(a, k, false);
+                const int64_t w = (int64_t)cl.units(a) * LH;
                 if (u < at + w) break;
                 at += w;
             }
@@ -356,66 +411,73 @@ __global__ void __launch_bounds__(KA_THREADS, 2) k_kv_attn(const __grid_constant
     const int64_t n_units = (total + gridDim.x - 1) / gridDim.x;
     int64_t u0 = blockIdx.x * n_units;
     const int64_t u1 = min(total, u0 + n_units);
-    if (tid == 0) a.split[blockIdx.x] = make_longlong2(-1, -1);
+    if (tid == 0) a.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
     if (u0 >= u1) return;
-    int64_t k, cls0;                                         // class, its first unit
+    int k;                                                   // class, its first unit
+    int64_t cls0;
     if (SEL) {
-        const int64_t w = cl.units(a) * LH;
-        k = u0 / w;
+        const int64_t w = (int64_t)cl.units(a) * LH;
+        k = (int)(u0 / w);
         cls0 = k * w;
     } else {
         k = sm.cls;
         cls0 = sm.off;
     }
-    cl.set(a, k, RPT, SEL && tid == 0);
-    int64_t per = cl.units(a);
+    cl.set(a, k, SEL && tid == 0);
+    int per = cl.units(a);
+    const int lh = (int)((u0 - cls0) / per);                 // line of the class, its first unit
+    int64_t line0 = cls0 + (int64_t)lh * per;
+    int l = lh / a.c.H, h = lh % a.c.H;
+    float *const my_o = reinterpret_cast<float *>(sm.ring[warp]);
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp]);
 
     while (u0 < u1) {
-        if (u0 >= cls0 + per * LH) {                         // next class
-            cls0 += per * LH;
-            cl.set(a, ++k, RPT, SEL && tid == 0);
-            per = cl.units(a);
-        }
-        const int64_t lh = (u0 - cls0) / per, line0 = cls0 + lh * per;
-        const int64_t s0 = u0 - line0, s1 = min(per, u1 - line0);   // this segment's units of the line
-        const int l = (int)(lh / a.c.H), h = (int)(lh % a.c.H);
+        const int s0 = (int)(u0 - line0), s1 = (int)min((int64_t)per, u1 - line0);   // this segment's units of the line
         const int64_t sh = (int64_t)cl.s * a.c.H + h;
         const KaLine<DT> ln{a.c.codes(l, sh, 0), a.c.codes(l, sh, 1), a.c.params(l, sh, 0), a.c.params(l, sh, 1)};
         const int32_t *sel = SEL ? a.sel + ((((int64_t)l * a.c.S + cl.s) * a.n_q + cl.i) * a.c.H + h) * a.n_sel : nullptr;
-        const int64_t v_end = min(cl.tiles(a), s1 * KA_WARPS);       // tiles [v, v_end) in steps of KA_WARPS
-        int64_t v = s0 * KA_WARPS + warp;
+        // tiles [v, v_end) in steps of KA_WARPS
+        const int v_end = min(cl.tiles(a), (s1 - KA_BEGIN) * KA_WARPS);
+        int v = max(s0 - KA_BEGIN, 0) * KA_WARPS + warp;
 
         // first token of tile v and the end of its rows
-        auto slot = [&](int64_t x) { return a.tpb_magic ? (int)__umulhi((uint32_t)x, a.tpb_magic) : (int)x; };
-        auto id_of = [&](int64_t x) { return x < v_end ? __ldg(sel + slot(x)) : -1; };
-        auto place = [&](int64_t x, int id, int64_t &t0, int64_t &end) {
+        auto slot = [&](int x) { return a.tpb_magic ? (int)__umulhi((uint32_t)x, a.tpb_magic) : x; };
+        auto id_of = [&](int x) { return x < v_end ? __ldg(sel + slot(x)) : -1; };
+        auto place = [&](int x, int id, int &t0, int &end) {
             if (SEL) {
                 const bool ok = id >= 0 && id < a.c.n_b;
                 if (!ok && id != -1 && lane == 0) raise_status(ST_BOUNDS);
-                t0 = ok ? ((int64_t)id * a.tpb + (x - (int64_t)slot(x) * a.tpb)) * 16 : 0;
+                t0 = ok ? (id * a.tpb + (x - slot(x) * a.tpb)) * 16 : 0;
                 end = ok ? cl.end : 0;
             } else {
-                t0 = x * 16;
+                t0 = x < v_end ? x * 16 : 0;
                 end = x < v_end ? cl.end : 0;
             }
         };
-        KaTile<DT> t;
-        int64_t t0, end;
-        int id_next = 0;
-        place(v, SEL ? id_of(v) : 0, t0, end);
-        if (SEL) id_next = id_of(v + KA_WARPS);
-        ka_load_k<DT>(t, ln, t0, end, g, c);
-        ka_load_v<DT>(t, ln, t0, end, g, c);
-
-        // the line's queries as fragments, a warp per row
-        for (int r = warp; r < RPT; r += KA_WARPS) {
-            float x[4] = {0.f, 0.f, 0.f, 0.f};
-            const bool live = r < cl.rows;
-            if (live) {
-                const T *q = (const T *)a.q + cl.row(a, l, h, r, RPT) * D + 4 * lane;
+        // first token and end of the tiles in flight
+        constexpr int AHEAD = Tl::STAGES - 1;
+        int t0[AHEAD], end[AHEAD], id_next = 0;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = to_f32(q[e]);
-            }
+        for (int i = 0; i < AHEAD; ++i) {
+            place(v + i * KA_WARPS, SEL ? id_of(v + i * KA_WARPS) : 0, t0[i], end[i]);
+            ka_fetch<DT>(ring + i * Tl::BYTES, ln, t0[i], end[i], lane);
+            ka_commit();
+        }
+        if (SEL) id_next = id_of(v + AHEAD * KA_WARPS);
+
+        // the line's queries as fragments, a warp per row (RPT / KA_WARPS rows each)
+        float qx[RPT / KA_WARPS][4];
+#pragma unroll
+        for (int y = 0; y < RPT / KA_WARPS; ++y) {
+            const int r = warp + y * KA_WARPS;
+            const T *q = (const T *)a.q + cl.row(a, l, h, min(r, cl.rows - 1)) * D + 4 * lane;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) qx[y][e] = r < cl.rows ? to_f32(q[e]) : 0.f;
+        }
+#pragma unroll
+        for (int y = 0; y < RPT / KA_WARPS; ++y) {
+            const int r = warp + y * KA_WARPS;
+            const float (&x)[4] = qx[y];
             float mx = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
             for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
             const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 127);
@@ -423,38 +485,28 @@ __global__ void __launch_bounds__(KA_THREADS, 2) k_kv_attn(const __grid_constant
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 const int ch = 4 * lane + w;
-                int j, cc, el;                                // the inverse of ka_channel
-                if (DT == MILO_INT4) {
-                    cc = ch / 32;
-                    j = 2 * ((ch % 32) / 8) + (ch % 4) / 2;
-                    el = 2 * (ch % 2) + (ch % 8) / 4;
-                } else {
-                    cc = (ch % 64) / 16;
-                    j = (ch / 64) * 4 + (ch % 16) / 4;
-                    el = ch % 4;
-                }
-                const float y = isfinite(x[w]) ? x[w] * up : NAN;   // an infinity spoils its row's scores like a NaN
-                const __half hi = __float2half_rn(y);
+                int j, cc, el;
+                ka_place<DT>(ch, j, cc, el);
+                const float z = isfinite(x[w]) ? x[w] * up : NAN;   // an infinity spoils its row's scores like a NaN
+                const __half hi = __float2half_rn(z);
                 __half *f = reinterpret_cast<__half *>(sm.q[r / 8][j][(r % 8) * 4 + cc]);
                 f[el] = hi;
-                if (PARTS == 2) f[4 + el] = __float2half_rn(y - __half2float(hi));
+                if (PARTS == 2) f[4 + el] = __float2half_rn(z - __half2float(hi));
             }
             if (lane == 0) {
                 sm.sc[r] = a.scale * (DT == MILO_FP8 ? KA_FP8_UP : 1.f) * down;
                 // rows behind the last are zero queries that see what the others see
-                sm.seen[r] = SEL || !live ? cl.end : kv_seen(a.len, cl.s, a.n_q, cl.query(a, r, RPT), a.c.cap, false);
+                sm.seen[r] = r < cl.rows ? cl.seen(a, r) : cl.end;
             }
         }
         __syncthreads();
         float sc[NT][2], ref[NT][2], sum[NT][2], o[NT][8][4];
-        int seen[NT][2], least = cl.end;                     // least: tokens that every row of the thread sees
+        const int least = cl.seen(a, 0);                // tokens that every row sees
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 sc[n][x] = sm.sc[8 * n + 2 * c + x];
-                seen[n][x] = sm.seen[8 * n + 2 * c + x];
-                least = min(least, seen[n][x]);
                 ref[n][x] = -INFINITY;
                 sum[n][x] = 0.f;
 #pragma unroll
@@ -462,55 +514,62 @@ __global__ void __launch_bounds__(KA_THREADS, 2) k_kv_attn(const __grid_constant
             }
         float e_max = 0.f, e_inv = 0.f;                      // 2^E and 2^-E of the value scales so far
 
+        int stage = 0;
         for (; v < v_end; v += KA_WARPS) {
-            int64_t t0n, endn;
-            place(v + KA_WARPS, id_next, t0n, endn);
-            if (SEL) id_next = id_of(v + 2 * KA_WARPS);
-            // scores: tokens t0 + g (+ 8), queries 2c, 2c + 1 of each tile of 8
-            float s[NT][4], slo[NT][4];
+            ka_wait<AHEAD - 1>();
+            __syncwarp();                                    // this tile is there, and the one before it used
+            int t0n, endn;
+            place(v + AHEAD * KA_WARPS, id_next, t0n, endn);
+            if (SEL) id_next = id_of(v + (AHEAD + 1) * KA_WARPS);
+            ka_fetch<DT>(ring + (stage == 0 ? AHEAD : stage - 1) * Tl::BYTES, ln, t0n, endn, lane);
+            ka_commit();
+            const unsigned char *st = sm.ring[warp] + stage * Tl::BYTES;
+            stage = stage == AHEAD ? 0 : stage + 1;
+            // scores: tokens ka_token(g) and ka_token(g + 8), queries 2c, 2c + 1 of each tile of 8
+            float s[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) s[n][x] = slo[n][x] = 0.f;
+                for (int x = 0; x < 4; ++x) s[n][x] = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t f[4];
-                ka_frag_k<DT>(t, j, f);
+            for (int y = 0; y < 2; ++y) {
+                uint32_t f[4][4];
+                ka_frag_k<DT>(st, y, g, c, f);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if constexpr (PARTS == 2) {
-                        const uint4 b = *reinterpret_cast<const uint4 *>(sm.q[n][j][lane]);
-                        ka_mma(s[n], f[0], f[1], f[2], f[3], b.x, b.y);
-                        ka_mma(slo[n], f[0], f[1], f[2], f[3], b.z, b.w);
-                    } else {
-                        const uint2 b = *reinterpret_cast<const uint2 *>(sm.q[n][j][lane]);
-                        ka_mma(s[n], f[0], f[1], f[2], f[3], b.x, b.y);
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        if constexpr (PARTS == 2) {
+                            const uint4 b = *reinterpret_cast<const uint4 *>(sm.q[n][4 * y + j][lane]);
+                            ka_mma(s[n], f[j][0], f[j][1], f[j][2], f[j][3], b.x, b.y);
+                            ka_mma(s[n], f[j][0], f[j][1], f[j][2], f[j][3], b.z, b.w);
+                        } else {
+                            const uint2 b = *reinterpret_cast<const uint2 *>(sm.q[n][4 * y + j][lane]);
+                            ka_mma(s[n], f[j][0], f[j][1], f[j][2], f[j][3], b.x, b.y);
+                        }
                     }
-                }
             }
             float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
             if constexpr (PAR) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    ks[r] = t.ks[r];
-                    vs[r] = t.vs[r];
+                    ks[r] = *reinterpret_cast<const float *>(st + Tl::KP + 4 * (g + 8 * r));
+                    vs[r] = *reinterpret_cast<const float *>(st + Tl::VP + 4 * (g + 8 * r));
                 }
             }
-            ka_load_k<DT>(t, ln, t0n, endn, g, c);
             bool raise = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    if (PARTS == 2) s[n][x] += slo[n][x];
                     s[n][x] *= PAR ? ks[x / 2] * sc[n][x % 2] : sc[n][x % 2];
                 }
-            if (t0 + 16 > least || end == 0) {
+            if (t0[0] + 16 > least || end[0] == 0) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
-                        if (t0 + g + 8 * (x / 2) >= min((int64_t)seen[n][x % 2], end)) s[n][x] = -INFINITY;
+                        if (t0[0] + ka_token<DT>(g + 8 * (x / 2)) >= min(sm.seen[8 * n + 2 * c + x % 2], end[0])) s[n][x] = -INFINITY;
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -573,10 +632,12 @@ __global__ void __launch_bounds__(KA_THREADS, 2) k_kv_attn(const __grid_constant
                                                                          p[2 * r + 1] - __high2float(hi))));
                 }
             }
+            KaValues<DT> vals;
+            ka_read_v<DT>(st, g, c, vals);
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 uint32_t f[2][4];
-                ka_frag_v<DT>(t, w, f);
+                ka_frag_v<DT>(vals, w, f);
 #pragma unroll
                 for (int y = 0; y < 2; ++y)
 #pragma unroll
@@ -585,10 +646,16 @@ __global__ void __launch_bounds__(KA_THREADS, 2) k_kv_attn(const __grid_constant
                         for (int p = 0; p < PARTS; ++p)
                             ka_mma(o[n][2 * w + y], f[y][0], f[y][1], f[y][2], f[y][3], b[n][0][p], b[n][1][p]);
             }
-            ka_load_v<DT>(t, ln, t0n, endn, g, c);
-            t0 = t0n;
-            end = endn;
+#pragma unroll
+            for (int i = 0; i + 1 < AHEAD; ++i) {
+                t0[i] = t0[i + 1];
+                end[i] = end[i + 1];
+            }
+            t0[AHEAD - 1] = t0n;
+            end[AHEAD - 1] = endn;
         }
+        ka_wait<0>();
+        __syncwarp();                                        // the ring is free: the warp's output goes there
 
         // join the warps: reference and sum per query, then the outputs
 #pragma unroll
@@ -604,91 +671,144 @@ __global__ void __launch_bounds__(KA_THREADS, 2) k_kv_attn(const __grid_constant
                 }
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
-                    *reinterpret_cast<float4 *>(&sm.o[warp][r][16 * g + 4 * w]) =
+                    *reinterpret_cast<float4 *>(my_o + r * (D + 4) + 16 * g + 4 * w) =
                         make_float4(o[n][2 * w][x], o[n][2 * w][2 + x], o[n][2 * w + 1][x], o[n][2 * w + 1][2 + x]);
             }
         if (lane == 0) sm.e[warp] = PAR ? e_max : 1.f;
         __syncthreads();
         const bool whole = s0 == 0 && s1 == per;
         const int64_t part = 2 * (int64_t)blockIdx.x + (s0 == 0 ? 1 : 0);
-        float e_top = 0.f;
-#pragma unroll
-        for (int w = 0; w < KA_WARPS; ++w) e_top = fmaxf(e_top, sm.e[w]);
-        for (int x = tid; x < RPT * D; x += KA_THREADS) {
-            const int r = x / D, ch = x % D;
-            if (r >= cl.rows) break;
-            float m = -INFINITY, num = 0.f, den = 0.f;
-#pragma unroll
-            for (int w = 0; w < KA_WARPS; ++w) m = fmaxf(m, sm.m[w][r]);
+        if (tid < RPT) {                                     // each warp's share of a row
+            float e_top = 0.f, m = -INFINITY, den = 0.f;
 #pragma unroll
             for (int w = 0; w < KA_WARPS; ++w) {
-                if (sm.m[w][r] == -INFINITY && sm.l[w][r] == 0.f) continue;      // saw nothing
-                const float f = ka_exp2(sm.m[w][r] - m);
-                den = fmaf(f, sm.l[w][r], den);
-                num = fmaf(f * (e_top > 0.f ? sm.e[w] / e_top : 0.f), sm.o[w][r][ch], num);
+                e_top = fmaxf(e_top, sm.e[w]);
+                m = fmaxf(m, sm.m[w][tid]);
             }
-            const float y = den != 0.f ? num / den * (e_top * (DT == MILO_FP8 ? KA_FP8_UP : 1.f)) : 0.f;
-            if (whole) ka_finish<T>(a, cl.row(a, l, h, r, RPT), ch, y, m - KA_SHIFT, den);
+            float f[KA_WARPS];
+#pragma unroll
+            for (int w = 0; w < KA_WARPS; ++w) {
+                f[w] = sm.l[w][tid] != 0.f ? ka_exp2(sm.m[w][tid] - m) : 0.f;   // 0: saw nothing
+                den = fmaf(f[w], sm.l[w][tid], den);
+            }
+            const float inv = den != 0.f ? 1.f / den : 0.f, down = e_top > 0.f ? 1.f / e_top : 0.f;
+#pragma unroll
+            for (int w = 0; w < KA_WARPS; ++w) sm.m[w][tid] = f[w] * inv * (sm.e[w] * down);
+            sm.l[0][tid] = den;
+            sm.sc[tid] = m - KA_SHIFT;
+            if (tid == 0) sm.e[KA_WARPS] = e_top * (DT == MILO_FP8 ? KA_FP8_UP : 1.f);
+        }
+        __syncthreads();
+        for (int r = warp; r < cl.rows; r += KA_WARPS) {     // a row per warp, four channels a lane
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < KA_WARPS; ++w) {
+                const float f = sm.m[w][r];
+                const float4 x = *reinterpret_cast<const float4 *>(sm.ring[w] + (r * (D + 4) + 4 * lane) * 4);
+                y.x = fmaf(f, x.x, y.x);
+                y.y = fmaf(f, x.y, y.y);
+                y.z = fmaf(f, x.z, y.z);
+                y.w = fmaf(f, x.w, y.w);
+            }
+            const float up = sm.e[KA_WARPS];
+            y = make_float4(y.x * up, y.y * up, y.z * up, y.w * up);
+            if (whole) ka_finish<T>(a, cl.row(a, l, h, r), lane, y, sm.sc[r], sm.l[0][r]);
             else {
-                a.part_o[(part * RPT + r) * D + ch] = y;
-                if (ch == 0) a.part_ml[part * RPT + r] = make_float2(m - KA_SHIFT, den);
+                *reinterpret_cast<float4 *>(a.part_o + (part * RPT + r) * D + 4 * lane) = y;
+                if (lane == 0) a.part_ml[part * RPT + r] = make_float2(sm.sc[r], sm.l[0][r]);
             }
         }
         if (!whole && s0 == 0 && tid == 0)                   // begun here, ended by a later CTA
-            a.split[blockIdx.x] = make_longlong2(k * LH + lh, (line0 + per - 1) / n_units);
+            a.split[blockIdx.x] = make_int4(k, l, h, (int)((line0 + per - 1) / n_units));
         __syncthreads();                                     // queries and outputs used before the next segment
         u0 = line0 + s1;
+        if (s1 == per) {                                     // next line
+            line0 += per;
+            if (++h == a.c.H) {
+                h = 0;
+                if (++l == a.c.L) {
+                    l = 0;
+                    if (u0 < u1) {
+                        ++k;
+                        cl.next(a, SEL && tid == 0);
+                        per = cl.units(a);
+                    }
+                }
+            }
+        }
     }
 }
 
-// Joins the parts of a line that CTA blockIdx.x begins: grid (grid of k_kv_attn, 8 NT rows),
-// 16 warps take the parts in turn.
+// Joins the parts of a line that CTA blockIdx.x begins, in their order.  Each of
+// the gridDim.y CTAs takes 8 NT / gridDim.y of its rows, and the 16 / that many
+// warps of a row take its parts in turn.
 constexpr int KA_MERGE_WARPS = 16;
 template <typename T, int NT, bool SEL>
 __global__ void __launch_bounds__(32 * KA_MERGE_WARPS) k_kv_attn_merge(const __grid_constant__ KvAttnArgs a) {
     constexpr int RPT = 8 * NT;
     __shared__ float s_o[KA_MERGE_WARPS][D], s_l[KA_MERGE_WARPS], s_m[KA_MERGE_WARPS];
-    const longlong2 sp = a.split[blockIdx.x];
+    const int4 sp = a.split[blockIdx.x];
     if (sp.x < 0) return;
-    const int64_t LH = (int64_t)a.c.L * a.c.H, lh = sp.x % LH;
-    const int r = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    KaClass<SEL> cl;
-    cl.set(a, sp.x / LH, RPT, false);
-    if (r >= cl.rows) return;
-    const int n = (int)(sp.y - blockIdx.x) + 1;              // parts: slot 1 of the first CTA, slot 0 of the others
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = RPT / gridDim.y, wpr = KA_MERGE_WARPS / per;     // rows of this CTA, warps of a row
+    const int r = blockIdx.y * per + warp / wpr, w0 = warp % wpr;
+    KaClass<SEL, NT> cl;
+    cl.set(a, sp.x, false);
+    const int n = sp.w - (int)blockIdx.x + 1;                // parts: slot 1 of the first CTA, slot 0 of the others
     auto at = [&](int i) { return (2 * ((int64_t)blockIdx.x + i) + (i == 0)) * RPT + r; };
-    float m = -INFINITY;
-    for (int i = tid; i < n; i += 32 * KA_MERGE_WARPS) {
-        const float2 x = a.part_ml[at(i)];
-        if (x.y != 0.f) m = fmaxf(m, x.x);
-    }
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) s_m[warp] = m;
-    __syncthreads();
-    for (int w = 0; w < KA_MERGE_WARPS; ++w) m = fmaxf(m, s_m[w]);
+    float m = -INFINITY, den = 0.f;
     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-    float den = 0.f;
-#pragma unroll 4
-    for (int i = warp; i < n; i += KA_MERGE_WARPS) {
-        const float2 x = a.part_ml[at(i)];
-        const float4 o = *reinterpret_cast<const float4 *>(a.part_o + at(i) * D + 4 * lane);
-        const float w = x.y != 0.f ? ka_exp2(x.x - m) * x.y : 0.f;
-        den += w;
-        num.x = fmaf(w, o.x, num.x);
-        num.y = fmaf(w, o.y, num.y);
-        num.z = fmaf(w, o.z, num.z);
-        num.w = fmaf(w, o.w, num.w);
+    constexpr int BATCH = 4;
+    for (int i0 = w0; i0 < n; i0 += BATCH * wpr) {
+        float2 x[BATCH];
+        float4 o[BATCH];
+#pragma unroll
+        for (int y = 0; y < BATCH; ++y) {
+            const int i = i0 + y * wpr;
+            x[y] = make_float2(-INFINITY, 0.f);
+            o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < n) {
+                x[y] = a.part_ml[at(i)];
+                o[y] = *reinterpret_cast<const float4 *>(a.part_o + at(i) * D + 4 * lane);
+            }
+        }
+        float top = m;
+#pragma unroll
+        for (int y = 0; y < BATCH; ++y)
+            if (x[y].y != 0.f) top = fmaxf(top, x[y].x);
+        const float f = den != 0.f ? ka_exp2(m - top) : 0.f;
+        m = top;
+        den *= f;
+        num = make_float4(num.x * f, num.y * f, num.z * f, num.w * f);
+#pragma unroll
+        for (int y = 0; y < BATCH; ++y) {
+            const float w = x[y].y != 0.f ? ka_exp2(x[y].x - m) * x[y].y : 0.f;
+            den += w;
+            num.x = fmaf(w, o[y].x, num.x);
+            num.y = fmaf(w, o[y].y, num.y);
+            num.z = fmaf(w, o[y].z, num.z);
+            num.w = fmaf(w, o[y].w, num.w);
+        }
     }
+    if (lane == 0) s_m[warp] = m;
     *reinterpret_cast<float4 *>(&s_o[warp][4 * lane]) = num;
     if (lane == 0) s_l[warp] = den;
     __syncthreads();
-    if (tid < D) {
-        float y = 0.f, d = 0.f;
-        for (int w = 0; w < KA_MERGE_WARPS; ++w) {
-            y += s_o[w][tid];
-            d += s_l[w];
+    if (w0 == 0 && r < cl.rows) {
+        float top = m;
+        for (int w = 1; w < wpr; ++w) top = fmaxf(top, s_m[warp + w]);
+        num = make_float4(0.f, 0.f, 0.f, 0.f);
+        den = 0.f;
+        for (int w = 0; w < wpr; ++w) {
+            const float4 o = *reinterpret_cast<const float4 *>(&s_o[warp + w][4 * lane]);
+            const float f = s_l[warp + w] != 0.f ? ka_exp2(s_m[warp + w] - top) : 0.f;
+            num = make_float4(fmaf(f, o.x, num.x), fmaf(f, o.y, num.y), fmaf(f, o.z, num.z), fmaf(f, o.w, num.w));
+            den = fmaf(f, s_l[warp + w], den);
         }
-        ka_finish<T>(a, cl.row(a, (int)(lh / a.c.H), (int)(lh % a.c.H), r, RPT), tid, d != 0.f ? y / d : 0.f, m, d);
+        m = top;
+        const float inv = den != 0.f ? 1.f / den : 0.f;
+        num = make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv);
+        ka_finish<T>(a, cl.row(a, sp.y, sp.z, r), lane, num, m, den);
     }
 }
 
