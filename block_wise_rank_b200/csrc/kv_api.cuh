@@ -159,6 +159,20 @@ KvAttnPlan kv_attn_plan(const milo_kv_shape *s, int32_t n_q, int32_t Hq, int32_t
     return p;
 }
 
+// Launch of a kernel that waits for its predecessor itself (kv_wait_previous).
+template <typename A> cudaError_t kv_follow(void (*kernel)(A), dim3 grid, int threads, const A &a, cudaStream_t s) {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3((unsigned)threads);
+    c.stream = s;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, a);
+}
+
 // opt-in shared memory of a kernel, once per device
 template <typename K> cudaError_t kv_smem(K kernel, size_t bytes, bool (&done)[64]) {
     int dev = 0;
@@ -177,8 +191,11 @@ template <typename T, int DT, int NT, bool SEL> cudaError_t kv_attn_run(const Kv
     k_kv_attn<T, DT, NT, SEL><<<grid, 32 * KaShape<NT>::WARPS, smem, s>>>(a);
     // many parts a line: a CTA per row, else one for the line
     const int64_t lines = (int64_t)a.classes * a.c.L * a.c.H;
-    if (grid > 1)
-        k_kv_attn_merge<T, NT, SEL><<<dim3(grid, grid >= 16 * lines ? 8 * NT : 1), 32 * KA_MERGE_WARPS, 0, s>>>(a);
+    if (grid > 1) {
+        const cudaError_t m = kv_follow(k_kv_attn_merge<T, NT, SEL>, dim3(grid, grid >= 16 * lines ? 8 * NT : 1),
+                                        32 * KA_MERGE_WARPS, a, s);
+        if (m != cudaSuccess) return m;
+    }
     return cudaGetLastError();
 }
 
@@ -202,7 +219,6 @@ milo_status kv_attn_launch(const milo_kv_shape *shape, const void *cache, const 
     a.q = q; a.out = out; a.lse = lse; a.ml = ml; a.len = len; a.sel = selected;
     a.n_q = n_q; a.G = Hq / shape->H; a.n_sel = n_sel;
     a.tpb = shape->block_len / 16;
-    a.tpb_magic = a.tpb == 1 ? 0u : (uint32_t)(((1ull << 32) + a.tpb - 1) / a.tpb);
     a.row_tiles = p.row_tiles; a.classes = p.classes;
     a.scale = (float)((scale > 0.0 ? scale : 1.0 / std::sqrt((double)D)) * 1.4426950408889634074);
     a.part_o = (float *)((char *)workspace + p.part_o);
@@ -403,9 +419,10 @@ milo_status milo_kv_select(const milo_kv_shape *shape, const void *cache, size_t
     cudaEvent_t t0 = tmark(s);
     if (q_dtype == MILO_BF16) k_kv_score<__nv_bfloat16><<<grid, KV_SCORE_THREADS, 0, s>>>(a);
     else k_kv_score<float><<<grid, KV_SCORE_THREADS, 0, s>>>(a);
-    k_kv_topn<<<rows, KV_TOPN_THREADS, 0, s>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = kv_follow(k_kv_topn, dim3(rows), KV_TOPN_THREADS, a, s);
     tpush(MILO_TK_KV_SELECT, t0, tmark(s));
-    return cuda_check(cudaGetLastError(), "kv select launch");
+    return cuda_check(e, "kv select launch");
 }
 
 size_t milo_kv_attn_workspace_size(const milo_kv_shape *shape, int32_t n_q, int32_t Hq, int32_t n_sel) {

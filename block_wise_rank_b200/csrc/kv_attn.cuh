@@ -44,7 +44,6 @@ struct KvAttnArgs {
     const int32_t *sel;            // [L][S][n_q][H][n_sel] or null
     int n_q, G, n_sel;
     int tpb;                       // tiles of 16 tokens per block
-    uint32_t tpb_magic;            // ceil(2^32 / tpb), 0 for tpb = 1
     int row_tiles;                 // query tiles of a line's rows
     int classes;                   // S * row_tiles (dense), S * n_q * row_tiles (selected)
     float scale;                   // softmax scale * log2(e)
@@ -94,19 +93,18 @@ __device__ __forceinline__ uint32_t ka_fp8(uint32_t x, uint32_t sel) {
     const uint32_t w = __byte_perm(x, 0u, sel);
     return (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
 }
-// two codes of 4 bits in bits 0-3 (HI: 4-7) of a word's halves -> their fp16 values
+// two codes of 4 bits in bits 0-3 (HI: 4-7) of a word's halves -> their fp16 values: the codes under the
+// exponent whose last place is worth 1 (1024 + code), or 2^-4 (64 + code)
 template <bool HI> __device__ __forceinline__ uint32_t ka_int4(uint32_t x, __half2 s, __half2 z) {
-    __half2 c;
-    if (HI) c = __hfma2(ka_h((x & 0x00f000f0u) | 0x64006400u), __half2half2(__ushort_as_half(0x2c00)),
-                        __half2half2(__ushort_as_half(0xd400)));    // (1024 + 16 code) / 16 - 64
-    else c = __hsub2(ka_h((x & 0x000f000fu) | 0x64006400u), __half2half2(__ushort_as_half(0x6400)));
-    return ka_u(__hfma2(c, s, z));
+    uint32_t w;   // (x & mask) | exponent in one instruction
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(w) : "r"(x), "n"(HI ? 0x00f000f0 : 0x000f000f), "r"(HI ? 0x54005400 : 0x64006400));
+    return ka_u(__hfma2(__hsub2(ka_h(w), __half2half2(__ushort_as_half(HI ? 0x5400 : 0x6400))), s, z));
 }
 
 // ---------------------------------------------------------- a tile's codes
 // A warp's ring in shared memory holds a tile of 16 tokens per stage: keys,
-// values, then the parameters, brought by 16-byte asynchronous copies (rows from
-// `end` on are filled with zeros and not read; t0 is a row of the line).  Row r of the score product is
+// values, then the parameters, brought by 16-byte asynchronous copies (rows behind the
+// first `rem` are filled with zeros and not read; t0 is a row of the line).  Row r of the score product is
 // token ka_token(r) of the tile, and so is index r of the value product; that
 // and the exchange of 16-byte chunks below let the fragments' reads touch every bank
 // once.
@@ -130,31 +128,45 @@ template <int DT> __device__ __forceinline__ int ka_chunk(int t, int c) {
 __device__ __forceinline__ void ka_copy16(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void ka_copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void ka_copy4(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ void ka_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void ka_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// rows t0 .. t0 + 15 of a line into the stage at shared address `dst`
+// rows t0 .. t0 + min(rem, 16) - 1 of a line into the stage at shared address `dst`
 template <int DT>
-__device__ __forceinline__ void ka_fetch(uint32_t dst, const KaLine<DT> &ln, int t0, int end, int lane) {
+__device__ __forceinline__ void ka_fetch(uint32_t dst, const KaLine<DT> &ln, int t0, int rem, int lane) {
     using Tl = KaTile<DT>;
     constexpr int PER = Tl::ROW / 16, STEP = 32 / PER;       // chunks of a row, rows per round of the warp
-    const int c = lane % PER, r0 = lane / PER, rem = end - t0;
-    const int64_t at = (int64_t)t0 * Tl::ROW + (r0 * Tl::ROW + 16 * c);
+    const int c = lane % PER, r0 = lane / PER, rp = lane & 15;
+    const unsigned char *k = ln.k + ((int64_t)t0 * Tl::ROW + (r0 * Tl::ROW + 16 * c)), *v = k + (ln.v - ln.k);
+    const unsigned char *p = (lane < 16 ? ln.kp : ln.vp) + ((int64_t)t0 * Tl::PAR + rp * Tl::PAR);
+    const uint32_t top = dst + (lane < 16 ? Tl::KP : Tl::VP) + rp * Tl::PAR;
+    if (rem >= 16) {
+#pragma unroll
+        for (int i = 0; i < 16 / STEP; ++i) {
+            const int r = r0 + STEP * i;
+            const uint32_t to = dst + r * Tl::ROW + 16 * ka_chunk<DT>(r, c);
+            ka_copy16(to, k + STEP * i * Tl::ROW);
+            ka_copy16(to + Tl::V, v + STEP * i * Tl::ROW);
+        }
+        if (DT == MILO_INT4) ka_copy16(top, p);
+        else ka_copy4(top, p, true);
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < 16 / STEP; ++i) {
         const int r = r0 + STEP * i;
         const uint32_t to = dst + r * Tl::ROW + 16 * ka_chunk<DT>(r, c);
-        ka_copy16(to, ln.k + at + STEP * i * Tl::ROW, r < rem);
-        ka_copy16(to + Tl::V, ln.v + at + STEP * i * Tl::ROW, r < rem);
+        ka_copy16(to, k + STEP * i * Tl::ROW, r < rem);
+        ka_copy16(to + Tl::V, v + STEP * i * Tl::ROW, r < rem);
     }
-    const int r = lane & 15;
-    const unsigned char *p = (lane < 16 ? ln.kp : ln.vp) + ((int64_t)t0 * Tl::PAR + r * Tl::PAR);
-    const uint32_t to = dst + (lane < 16 ? Tl::KP : Tl::VP) + r * Tl::PAR;
-    if (DT == MILO_INT4) ka_copy16(to, p, r < rem);
-    else ka_copy4(to, p, r < rem);
+    if (DT == MILO_INT4) ka_copy16(top, p, rp < rem);
+    else ka_copy4(top, p, rp < rem);
 }
 
 // channel of element e (0..3: b0 low, b0 high, b1 low, b1 high) of the queries'
@@ -176,35 +188,49 @@ template <int DT> __device__ __forceinline__ void ka_place(int ch, int &j, int &
 
 __device__ __forceinline__ uint32_t ka_word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
-// The A fragments of four steps of the score product (half 0: steps 0-3, half 1: 4-7)
-template <int DT> __device__ __forceinline__ void ka_frag_k(const unsigned char *st, int half, int g, int c, uint32_t (&a)[4][4]) {
+// What a thread reads of the tile's keys: rows g and g + 8, 16-byte chunks c and c + 4 (4 bits: chunk c alone, with
+// the (scale, zero) of its group)
+template <int DT> struct KaKeys {
+    uint4 w[2][2];
+};
+template <> struct KaKeys<MILO_INT4> {
+    uint4 w[2];
+    uint32_t p[2];
+};
+template <int DT> __device__ __forceinline__ void ka_read_k(const unsigned char *st, int g, int c, KaKeys<DT> &k) {
     using Tl = KaTile<DT>;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
         const int t = ka_token<DT>(g + 8 * r);
+        const unsigned char *row = st + t * Tl::ROW;
         if constexpr (DT == MILO_INT4) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(st + t * Tl::ROW + 16 * ka_chunk<DT>(t, c) + 8 * half);
-            const uint32_t p = *reinterpret_cast<const uint32_t *>(st + Tl::KP + t * Tl::PAR + 4 * c);   // (scale, zero)
-            const __half2 s = ka_h(__byte_perm(p, 0u, 0x1010)), z = ka_h(__byte_perm(p, 0u, 0x3232));
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t x = (j < 2 ? w.x : w.y) >> (j % 2 ? 8 : 0);
-                a[j][r] = ka_int4<false>(x, s, z);
-                a[j][2 + r] = ka_int4<true>(x, s, z);
-            }
+            k.w[r] = *reinterpret_cast<const uint4 *>(row + 16 * ka_chunk<DT>(t, c));
+            k.p[r] = *reinterpret_cast<const uint32_t *>(st + Tl::KP + t * Tl::PAR + 4 * c);
         } else {
-            const uint4 w = *reinterpret_cast<const uint4 *>(st + t * Tl::ROW + 16 * ka_chunk<DT>(t, c + 4 * half));
+            k.w[r][0] = *reinterpret_cast<const uint4 *>(row + 16 * ka_chunk<DT>(t, c));
+            k.w[r][1] = *reinterpret_cast<const uint4 *>(row + 16 * ka_chunk<DT>(t, c + 4));
+        }
+    }
+}
+
+// A fragment of step j of the score product
+template <int DT> __device__ __forceinline__ void ka_frag_k(const KaKeys<DT> &k, int j, uint32_t (&a)[4]) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t x = ka_word(w, j);
-                if constexpr (DT == MILO_INT8) {
-                    x ^= 0x80808080u;
-                    a[j][r] = ka_int8(x, 0x4140);
-                    a[j][2 + r] = ka_int8(x, 0x4342);
-                } else {
-                    a[j][r] = ka_fp8(x, 0x1404);
-                    a[j][2 + r] = ka_fp8(x, 0x3424);
-                }
+    for (int r = 0; r < 2; ++r) {
+        if constexpr (DT == MILO_INT4) {
+            const __half2 s = ka_h(__byte_perm(k.p[r], 0u, 0x1010)), z = ka_h(__byte_perm(k.p[r], 0u, 0x3232));
+            const uint32_t x = ka_word(k.w[r], j / 2) >> (j % 2 ? 8 : 0);
+            a[r] = ka_int4<false>(x, s, z);
+            a[2 + r] = ka_int4<true>(x, s, z);
+        } else {
+            uint32_t x = ka_word(k.w[r][j / 4], j % 4);
+            if constexpr (DT == MILO_INT8) {
+                x ^= 0x80808080u;
+                a[r] = ka_int8(x, 0x4140);
+                a[2 + r] = ka_int8(x, 0x4342);
+            } else {
+                a[r] = ka_fp8(x, 0x1404);
+                a[2 + r] = ka_fp8(x, 0x3424);
             }
         }
     }
@@ -331,6 +357,7 @@ template <typename T, int DT, int NT> struct KaSmem {
     float e[KA_WARPS + 1];                                   // 2^E of the warps' value scales, and of the join
     float sc[RPT];                                           // factor on a row's scores
     int seen[RPT];
+    int t0[KA_WARPS][KaTile<DT>::STAGES];                    // first token of the tile in each stage
     int64_t scan[KA_WARPS + 1];
     int cls;
     int64_t off;
@@ -412,6 +439,7 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
     int64_t u0 = blockIdx.x * n_units;
     const int64_t u1 = min(total, u0 + n_units);
     if (tid == 0) a.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    kv_launch_next();
     if (u0 >= u1) return;
     int k;                                                   // class, its first unit
     int64_t cls0;
@@ -436,34 +464,50 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
         const int64_t sh = (int64_t)cl.s * a.c.H + h;
         const KaLine<DT> ln{a.c.codes(l, sh, 0), a.c.codes(l, sh, 1), a.c.params(l, sh, 0), a.c.params(l, sh, 1)};
         const int32_t *sel = SEL ? a.sel + ((((int64_t)l * a.c.S + cl.s) * a.n_q + cl.i) * a.c.H + h) * a.n_sel : nullptr;
-        // tiles [v, v_end) in steps of KA_WARPS
-        const int v_end = min(cl.tiles(a), (s1 - KA_BEGIN) * KA_WARPS);
-        int v = max(s0 - KA_BEGIN, 0) * KA_WARPS + warp;
-
-        // first token of tile v and the end of its rows
-        auto slot = [&](int x) { return a.tpb_magic ? (int)__umulhi((uint32_t)x, a.tpb_magic) : x; };
-        auto id_of = [&](int x) { return x < v_end ? __ldg(sel + slot(x)) : -1; };
-        auto place = [&](int x, int id, int &t0, int &end) {
-            if (SEL) {
-                const bool ok = id >= 0 && id < a.c.n_b;
-                if (!ok && id != -1 && lane == 0) raise_status(ST_BOUNDS);
-                t0 = ok ? (id * a.tpb + (x - slot(x) * a.tpb)) * 16 : 0;
-                end = ok ? cl.end : 0;
-            } else {
-                t0 = x < v_end ? x * 16 : 0;
-                end = x < v_end ? cl.end : 0;
-            }
+        // the segment's tiles, an equal run of them to each warp: `left` of them, fetched a few ahead of their use
+        const int first = max(s0 - KA_BEGIN, 0) * KA_WARPS;
+        const int tiles = max(min(cl.tiles(a), (s1 - KA_BEGIN) * KA_WARPS) - first, 0);
+        const int mine0 = first + (int)((int64_t)tiles * warp / KA_WARPS);
+        int left = first + (int)((int64_t)tiles * (warp + 1) / KA_WARPS) - mine0;
+        int to_fetch = left, t_next = 16 * mine0;            // selected: block `id`, its tile `in`, the block after it
+        int in = 0, slot = 0, id = -1, id_next = -1;
+        auto block_at = [&](int x) {
+            const int b = x < a.n_sel ? __ldg(sel + x) : -1;
+            if (b >= 0 && b < a.c.n_b) return b;
+            if (b != -1 && lane == 0) raise_status(ST_BOUNDS);
+            return -1;
         };
-        // first token and end of the tiles in flight
-        constexpr int AHEAD = Tl::STAGES - 1;
-        int t0[AHEAD], end[AHEAD], id_next = 0;
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            place(v + i * KA_WARPS, SEL ? id_of(v + i * KA_WARPS) : 0, t0[i], end[i]);
-            ka_fetch<DT>(ring + i * Tl::BYTES, ln, t0[i], end[i], lane);
-            ka_commit();
+        if (SEL) {
+            slot = mine0 / a.tpb;
+            in = mine0 - slot * a.tpb;
+            id = left > 0 ? block_at(slot) : -1;
+            id_next = left > a.tpb - in ? block_at(slot + 1) : -1;
         }
-        if (SEL) id_next = id_of(v + AHEAD * KA_WARPS);
+        constexpr int AHEAD = Tl::STAGES - 1, NONE = 0x7fffff00;
+        auto fetch = [&](int stage) {
+            int t0 = NONE;                                   // no tokens: every row is masked
+            if (to_fetch > 0) {
+                if (!SEL) {
+                    t0 = t_next;
+                    t_next += 16;
+                } else {
+                    if (id >= 0) t0 = (id * a.tpb + in) * 16;
+                    if (++in == a.tpb) {
+                        in = 0;
+                        id = id_next;
+                        ++slot;
+                        id_next = to_fetch - 1 > a.tpb ? block_at(slot + 1) : -1;
+                    }
+                }
+                --to_fetch;
+            }
+            const bool any = t0 < cl.end;
+            ka_fetch<DT>(ring + stage * Tl::BYTES, ln, any ? t0 : 0, any ? cl.end - t0 : 0, lane);
+            if (lane == 0) sm.t0[warp][stage] = any ? t0 : NONE;
+            ka_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i) fetch(i);
 
         // the line's queries as fragments, a warp per row (RPT / KA_WARPS rows each)
         float qx[RPT / KA_WARPS][4];
@@ -500,30 +544,26 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
             }
         }
         __syncthreads();
-        float sc[NT][2], ref[NT][2], sum[NT][2], o[NT][8][4];
+        float sc[NT][2], off[NT][2], sum[NT][2], o[NT][8][4];   // off: KA_SHIFT - reference
         const int least = cl.seen(a, 0);                // tokens that every row sees
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 sc[n][x] = sm.sc[8 * n + 2 * c + x];
-                ref[n][x] = -INFINITY;
+                off[n][x] = INFINITY;
                 sum[n][x] = 0.f;
 #pragma unroll
                 for (int w = 0; w < 8; ++w) o[n][w][2 * x] = o[n][w][2 * x + 1] = 0.f;
             }
         float e_max = 0.f, e_inv = 0.f;                      // 2^E and 2^-E of the value scales so far
 
-        int stage = 0;
-        for (; v < v_end; v += KA_WARPS) {
+        for (int stage = 0; left > 0; --left) {
             ka_wait<AHEAD - 1>();
             __syncwarp();                                    // this tile is there, and the one before it used
-            int t0n, endn;
-            place(v + AHEAD * KA_WARPS, id_next, t0n, endn);
-            if (SEL) id_next = id_of(v + (AHEAD + 1) * KA_WARPS);
-            ka_fetch<DT>(ring + (stage == 0 ? AHEAD : stage - 1) * Tl::BYTES, ln, t0n, endn, lane);
-            ka_commit();
+            fetch(stage == 0 ? AHEAD : stage - 1);
             const unsigned char *st = sm.ring[warp] + stage * Tl::BYTES;
+            const int t0 = sm.t0[warp][stage];
             stage = stage == AHEAD ? 0 : stage + 1;
             // scores: tokens ka_token(g) and ka_token(g + 8), queries 2c, 2c + 1 of each tile of 8
             float s[NT][4];
@@ -531,23 +571,23 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) s[n][x] = 0.f;
+            KaKeys<DT> keys;
+            ka_read_k<DT>(st, g, c, keys);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-                uint32_t f[4][4];
-                ka_frag_k<DT>(st, y, g, c, f);
+            for (int j = 0; j < 8; ++j) {
+                uint32_t f[4];
+                ka_frag_k<DT>(keys, j, f);
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if constexpr (PARTS == 2) {
-                            const uint4 b = *reinterpret_cast<const uint4 *>(sm.q[n][4 * y + j][lane]);
-                            ka_mma(s[n], f[j][0], f[j][1], f[j][2], f[j][3], b.x, b.y);
-                            ka_mma(s[n], f[j][0], f[j][1], f[j][2], f[j][3], b.z, b.w);
-                        } else {
-                            const uint2 b = *reinterpret_cast<const uint2 *>(sm.q[n][4 * y + j][lane]);
-                            ka_mma(s[n], f[j][0], f[j][1], f[j][2], f[j][3], b.x, b.y);
-                        }
+                for (int n = 0; n < NT; ++n) {
+                    if constexpr (PARTS == 2) {
+                        const uint4 b = *reinterpret_cast<const uint4 *>(sm.q[n][j][lane]);
+                        ka_mma(s[n], f[0], f[1], f[2], f[3], b.x, b.y);
+                        ka_mma(s[n], f[0], f[1], f[2], f[3], b.z, b.w);
+                    } else {
+                        const uint2 b = *reinterpret_cast<const uint2 *>(sm.q[n][j][lane]);
+                        ka_mma(s[n], f[0], f[1], f[2], f[3], b.x, b.y);
                     }
+                }
             }
             float ks[2] = {1.f, 1.f}, vs[2] = {1.f, 1.f};
             if constexpr (PAR) {
@@ -557,35 +597,35 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
                     vs[r] = *reinterpret_cast<const float *>(st + Tl::VP + 4 * (g + 8 * r));
                 }
             }
+            // exponents of the weights, relative to the references
+            float y[NT][4];
             bool raise = false;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    s[n][x] *= PAR ? ks[x / 2] * sc[n][x % 2] : sc[n][x % 2];
+                    const float f = PAR ? ks[x / 2] * sc[n][x % 2] : sc[n][x % 2];
+                    y[n][x] = fmaf(s[n][x], f, off[n][x % 2]);
+                    if (t0 + 16 > least && t0 + ka_token<DT>(g + 8 * (x / 2)) >= sm.seen[8 * n + 2 * c + x % 2])
+                        y[n][x] = -INFINITY;
+                    raise |= y[n][x] > KA_RAISE + KA_SHIFT;
                 }
-            if (t0[0] + 16 > least || end[0] == 0) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        if (t0[0] + ka_token<DT>(g + 8 * (x / 2)) >= min(sm.seen[8 * n + 2 * c + x % 2], end[0])) s[n][x] = -INFINITY;
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int x = 0; x < 4; ++x) raise |= s[n][x] > ref[n][x % 2] + KA_RAISE;
             if (__any_sync(0xffffffffu, raise)) {            // raise the references to this tile's maxima
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        float m = fmaxf(s[n][x], s[n][2 + x]);
+                        const float s0 = y[n][x] == -INFINITY ? -INFINITY : s[n][x] * (PAR ? ks[0] * sc[n][x] : sc[n][x]);
+                        const float s1 = y[n][2 + x] == -INFINITY ? -INFINITY : s[n][2 + x] * (PAR ? ks[1] * sc[n][x] : sc[n][x]);
+                        const float old = KA_SHIFT - off[n][x];
+                        float m = fmaxf(s0, s1);
 #pragma unroll
                         for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
-                        m = fmaxf(m, ref[n][x]);
-                        const float f = ref[n][x] == -INFINITY ? 0.f : ka_exp2(ref[n][x] - m);
-                        ref[n][x] = m;
+                        m = fmaxf(m, old);
+                        const float f = old == -INFINITY ? 0.f : ka_exp2(old - m);
+                        off[n][x] = KA_SHIFT - m;
+                        if (y[n][x] != -INFINITY) y[n][x] = s0 + off[n][x];
+                        if (y[n][2 + x] != -INFINITY) y[n][2 + x] = s1 + off[n][x];
                         sum[n][x] *= f;
 #pragma unroll
                         for (int w = 0; w < 8; ++w) {
@@ -618,8 +658,7 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
                 float p[4];
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const float m = ref[n][x % 2];
-                    p[x] = ka_exp2(s[n][x] - (m == -INFINITY ? 0.f : m) + KA_SHIFT);
+                    p[x] = ka_exp2(y[n][x]);
                     sum[n][x % 2] += p[x];
                     if (PAR) p[x] *= vs[x / 2];
                 }
@@ -646,13 +685,6 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
                         for (int p = 0; p < PARTS; ++p)
                             ka_mma(o[n][2 * w + y], f[y][0], f[y][1], f[y][2], f[y][3], b[n][0][p], b[n][1][p]);
             }
-#pragma unroll
-            for (int i = 0; i + 1 < AHEAD; ++i) {
-                t0[i] = t0[i + 1];
-                end[i] = end[i + 1];
-            }
-            t0[AHEAD - 1] = t0n;
-            end[AHEAD - 1] = endn;
         }
         ka_wait<0>();
         __syncwarp();                                        // the ring is free: the warp's output goes there
@@ -666,7 +698,7 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
                 for (int w = 4; w < 32; w <<= 1) sum[n][x] += __shfl_xor_sync(0xffffffffu, sum[n][x], w);
                 const int r = 8 * n + 2 * c + x;
                 if (g == 0) {
-                    sm.m[warp][r] = ref[n][x];
+                    sm.m[warp][r] = KA_SHIFT - off[n][x];
                     sm.l[warp][r] = sum[n][x];
                 }
 #pragma unroll
@@ -747,6 +779,7 @@ template <typename T, int NT, bool SEL>
 __global__ void __launch_bounds__(32 * KA_MERGE_WARPS) k_kv_attn_merge(const __grid_constant__ KvAttnArgs a) {
     constexpr int RPT = 8 * NT;
     __shared__ float s_o[KA_MERGE_WARPS][D], s_l[KA_MERGE_WARPS], s_m[KA_MERGE_WARPS];
+    kv_wait_previous();
     const int4 sp = a.split[blockIdx.x];
     if (sp.x < 0) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;

@@ -12,6 +12,12 @@
 
 namespace milo {
 
+// A kernel that follows another on its stream may be set up while that one
+// still runs (programmatic dependent launch): the first says that it can be, the
+// second waits for the first's end before it reads anything.
+__device__ __forceinline__ void kv_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void kv_wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 struct KvSelectArgs {
     KvView c;
     const void *q;                 // [L][S][n_q][Hq][D]
@@ -47,6 +53,7 @@ template <typename T> __global__ void __launch_bounds__(KV_SCORE_THREADS) k_kv_s
     const int cand = (seen + a.c.block_len - 1) / a.c.block_len;
     const int b = blockIdx.y * KV_SCORE_THREADS + tid;
     float best = -INFINITY;
+    kv_launch_next();
     for (int g0 = 0; g0 < a.G; g0 += KV_SCORE_G) {
         const int gn = min(KV_SCORE_G, a.G - g0);
         __syncthreads();
@@ -119,6 +126,7 @@ constexpr int KV_TOPN_THREADS = 256;
 // then the ids above it and the first of those equal to it, in order
 __global__ void __launch_bounds__(KV_TOPN_THREADS) k_kv_topn(KvSelectArgs a) {
     __shared__ int s_hist[256], s_gt[KV_TOPN_THREADS / 32], s_eq[KV_TOPN_THREADS / 32], s_bin, s_above;
+    kv_wait_previous();
     const int64_t row = blockIdx.x;
     const int64_t lsi = row / a.c.H;
     const int i = (int)(lsi % a.n_q), s = (int)((lsi / a.n_q) % a.c.S);
