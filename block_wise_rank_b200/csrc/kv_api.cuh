@@ -119,11 +119,18 @@ milo_status kv_query_check(const milo_kv_shape *s, const void *q, milo_dtype q_d
 // grid size for `ctas` thread blocks in x, 0 if there are too many
 unsigned grid_x(int64_t ctas) { return ctas > INT32_MAX ? 0u : (unsigned)ctas; }
 
-template <typename T> void kv_append_launch(const KvAppendArgs &a, unsigned grid, cudaStream_t s) {
-    const int threads = 32 * KV_APPEND_WARPS;
-    if (a.c.dtype == MILO_INT8) k_kv_append<T, MILO_INT8><<<grid, threads, 0, s>>>(a);
-    else if (a.c.dtype == MILO_FP8) k_kv_append<T, MILO_FP8><<<grid, threads, 0, s>>>(a);
-    else k_kv_append<T, MILO_INT4><<<grid, threads, 0, s>>>(a);
+template <typename T, int DT> void kv_append_run(const KvAppendArgs &a, cudaStream_t s) {
+    // up to four tokens are one step of a warp: a warp takes an item (28 layers x 8 sessions x 4 heads, one token)
+    if (a.n_new <= 4)
+        k_kv_append<T, DT, 1><<<(a.items + KV_APPEND_WARPS - 1) / KV_APPEND_WARPS, 32 * KV_APPEND_WARPS, 0, s>>>(a);
+    else
+        k_kv_append<T, DT, KV_APPEND_WARPS><<<a.items, 32 * KV_APPEND_WARPS, 0, s>>>(a);
+}
+
+template <typename T> void kv_append_launch(const KvAppendArgs &a, cudaStream_t s) {
+    if (a.c.dtype == MILO_INT8) kv_append_run<T, MILO_INT8>(a, s);
+    else if (a.c.dtype == MILO_FP8) kv_append_run<T, MILO_FP8>(a, s);
+    else kv_append_run<T, MILO_INT4>(a, s);
 }
 
 template <typename T> void kv_read_launch(const KvReadArgs &a, dim3 grid, cudaStream_t s) {
@@ -304,6 +311,7 @@ milo_status milo_rope(const milo_rope_params *p, const void *x, milo_dtype x_dty
     const int64_t per_head = n_tokens * a.units, wave = (int64_t)sm_count() * 2048;
     a.hpt = (int)std::min<int64_t>(n_heads, std::max<int64_t>(1, per_head * n_heads / wave));
     a.n_hc = (n_heads + a.hpt - 1) / a.hpt;
+    a.hpt = (n_heads + a.n_hc - 1) / a.n_hc;   // equal chunks
     if (grid_x((per_head * a.n_hc + 255) / 256) == 0) return MILO_ERR_UNSUPPORTED;
     cudaStream_t s = (cudaStream_t)stream;
     cudaEvent_t t0 = tmark(s);
@@ -356,12 +364,12 @@ milo_status milo_kv_append(const milo_kv_shape *shape, void *cache, size_t cache
         a.sl = strides[0]; a.ss = strides[1]; a.sh = strides[2]; a.st = strides[3];
     }
     a.windows = (int)(((int64_t)n_new - 2 + shape->block_len) / shape->block_len) + 1;
-    const unsigned grid = grid_x((int64_t)a.windows * shape->L * shape->S * shape->H * 2);
-    if (!grid) return MILO_ERR_UNSUPPORTED;
+    a.items = (int)grid_x((int64_t)a.windows * shape->L * shape->S * shape->H * 2);
+    if (!a.items) return MILO_ERR_UNSUPPORTED;
     cudaStream_t s = (cudaStream_t)stream;
     cudaEvent_t t0 = tmark(s);
-    if (in_dtype == MILO_BF16) kv_append_launch<__nv_bfloat16>(a, grid, s);
-    else kv_append_launch<float>(a, grid, s);
+    if (in_dtype == MILO_BF16) kv_append_launch<__nv_bfloat16>(a, s);
+    else kv_append_launch<float>(a, s);
     tpush(MILO_TK_KV_WRITE, t0, tmark(s));
     return cuda_check(cudaGetLastError(), "kv append launch");
 }
@@ -380,8 +388,8 @@ milo_status milo_kv_read(const milo_kv_shape *shape, const void *cache, size_t c
     KvReadArgs a{};
     a.c = kv_view(shape, cache);
     a.k = k_out; a.v = v_out; a.n = n; a.start = start; a.count = count;
-    a.rows = (int64_t)shape->L * shape->S * shape->H * n;
-    const unsigned grid = grid_x((a.rows * 8 + 255) / 256);
+    a.tiles = (n + KV_READ_ROWS - 1) / KV_READ_ROWS;
+    const unsigned grid = grid_x((int64_t)shape->L * shape->S * shape->H * a.tiles);
     if (!grid) return MILO_ERR_UNSUPPORTED;
     cudaStream_t s = (cudaStream_t)stream;
     cudaEvent_t t0 = tmark(s);
@@ -414,13 +422,20 @@ milo_status milo_kv_select(const milo_kv_shape *shape, const void *cache, size_t
     a.q = q; a.len = len; a.selected = selected; a.scores = scores ? scores : (float *)workspace;
     a.n_q = n_q; a.G = Hq / shape->H; a.n_sel = n_sel; a.n_first = n_first; a.n_last = n_last;
     const unsigned rows = grid_x((int64_t)shape->L * shape->S * n_q * shape->H);
-    const dim3 grid(rows, (unsigned)((a.c.n_b + KV_SCORE_THREADS - 1) / KV_SCORE_THREADS));
+    // blocks per CTA: as many steps of its warps as leave one wave of four CTAs an SM (a CTA first codes its queries, about
+    // what two steps cost)
+    const int64_t steps = (a.c.n_b + KV_SCORE_STEP - 1) / KV_SCORE_STEP, wave = 4 * sm_count();
+    const int per = KV_SCORE_STEP * (int)std::min<int64_t>((rows * steps + wave - 1) / wave, steps);
+    const dim3 grid(rows, (unsigned)((a.c.n_b + per - 1) / per));
     cudaStream_t s = (cudaStream_t)stream;
     cudaEvent_t t0 = tmark(s);
-    if (q_dtype == MILO_BF16) k_kv_score<__nv_bfloat16><<<grid, KV_SCORE_THREADS, 0, s>>>(a);
-    else k_kv_score<float><<<grid, KV_SCORE_THREADS, 0, s>>>(a);
+    if (q_dtype == MILO_BF16) k_kv_score<__nv_bfloat16><<<grid, 32 * KV_SCORE_WARPS, 0, s>>>(a, per);
+    else k_kv_score<float><<<grid, 32 * KV_SCORE_WARPS, 0, s>>>(a, per);
     cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) e = kv_follow(k_kv_topn, dim3(rows), KV_TOPN_THREADS, a, s);
+    if (e == cudaSuccess)
+        e = a.c.n_b <= 2048   ? kv_follow(k_kv_topn<256, 8, true>, dim3(rows), 256, a, s)
+            : a.c.n_b <= 8192 ? kv_follow(k_kv_topn<1024, 8, true>, dim3(rows), 1024, a, s)
+                              : kv_follow(k_kv_topn<1024, 1, false>, dim3(rows), 1024, a, s);
     tpush(MILO_TK_KV_SELECT, t0, tmark(s));
     return cuda_check(e, "kv select launch");
 }

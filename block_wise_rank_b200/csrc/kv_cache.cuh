@@ -45,15 +45,23 @@ __device__ __forceinline__ void kv_range(const int32_t *start, const int32_t *co
     }
 }
 
-// 16 consecutive elements as fp32
-template <typename T> __device__ __forceinline__ void kv_load16(const T *p, float (&x)[16]) {
-    constexpr int N = (int)sizeof(T);        // 16-byte vectors
-    uint4 w[N];
+// 16 consecutive elements, raw and as fp32
+template <typename T> struct KvRaw {
+    uint4 w[sizeof(T)];
+};
+template <typename T> __device__ __forceinline__ KvRaw<T> kv_raw16(const T *p) {
+    KvRaw<T> r;
 #pragma unroll
-    for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-    const T *e = reinterpret_cast<const T *>(w);
+    for (int i = 0; i < (int)sizeof(T); ++i) r.w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+    return r;
+}
+template <typename T> __device__ __forceinline__ void kv_f32(const KvRaw<T> &r, float (&x)[16]) {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(r.w);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = to_f32(e[i]);
+    for (int i = 0; i < 16; ++i) {
+        if constexpr (sizeof(T) == 4) x[i] = __uint_as_float(w[i]);
+        else x[i] = __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
 }
 
 template <typename T> __device__ __forceinline__ void kv_store16(T *p, const float (&x)[16]) {
@@ -69,11 +77,49 @@ template <typename T> __device__ __forceinline__ void kv_store16(T *p, const flo
     for (int i = 0; i < N; ++i) reinterpret_cast<uint4 *>(p)[i] = w[i];
 }
 
+// x / s rounded like an IEEE division, from inv = 1 / s rounded: by Markstein
+// ("Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990), one step q + (x - q s) inv of a quotient q within one place of x / s
+// rounds it correctly when the remainder is exact.  The first step brings x inv,
+// at most 1.5 places off, to within one.  Holds while no remainder that
+// matters for a code underflows: 2^-60 < s < 2^100 (|x| <= 448 s, codes from 2^-10 on).
+__device__ __forceinline__ float kv_quotient(float x, float s, float inv) {
+    float q = x * inv;
+    q = fmaf(fmaf(-q, s, x), inv, q);
+    return fmaf(fmaf(-q, s, x), inv, q);
+}
+__device__ __forceinline__ bool kv_plain_scale(float s) { return s > 0x1p-60f && s < 0x1p100f; }
+// x[i] / s for every i; 0 where s is 0
+template <int N> __device__ __forceinline__ void kv_divide(float (&x)[N], float s) {
+    if (kv_plain_scale(s)) {
+        const float inv = __frcp_rn(s);
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = kv_quotient(x[i], s, inv);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = s > 0.f ? __fdiv_rn(x[i], s) : 0.f;
+    }
+}
+constexpr float KV_MAGIC = 12582912.f;   // 1.5 * 2^23: the low bits of x + KV_MAGIC are the integer nearest to x, ties to even
+
+// the low bytes of four words
+__device__ __forceinline__ uint32_t kv_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+// INT8 codes of quotients within 127.5
+template <int N> __device__ __forceinline__ void kv_int8(const float (&q)[N], uint32_t (&w)[N / 4]) {
+    uint32_t r[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = __float_as_uint(q[i] + KV_MAGIC);
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) w[i] = kv_bytes(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+}
+
 // Quantise a lane's 16 channels (lane j of 8 holds channels 16 j ..) of one row
 // and store its codes and parameters.  All 8 lanes of the row call it together.
 template <int DT>
-__device__ __forceinline__ void kv_quant_store(const float (&x)[16], int j, unsigned mask, unsigned char *codes,
-                                               unsigned char *par) {
+__device__ __forceinline__ void kv_quant_store(const float (&x)[16], float amax, int j, unsigned mask,
+                                               unsigned char *codes, unsigned char *par) {
     if constexpr (DT == MILO_INT4) {
         float lo = x[0], hi = x[0];
 #pragma unroll
@@ -85,30 +131,38 @@ __device__ __forceinline__ void kv_quant_store(const float (&x)[16], int j, unsi
         hi = fmaxf(hi, __shfl_xor_sync(mask, hi, 1));
         const __half z = __float2half_rn(lo), s = __float2half_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
         const float zf = __half2float(z), sf = __half2float(s);
+        float q[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q[i] = __fsub_rn(x[i], zf);
+        kv_divide<16>(q, sf);
         uint32_t w[2] = {0u, 0u};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float c = sf > 0.f ? rintf(__fdiv_rn(__fsub_rn(x[i], zf), sf)) : 0.f;
-            w[i / 8] |= (uint32_t)fminf(fmaxf(c, 0.f), 15.f) << (4 * (i % 8));
-        }
+        for (int i = 0; i < 16; ++i)   // clamped before it is rounded: the same code, and within the trick's range
+            w[i / 8] |= (__float_as_uint(fminf(fmaxf(q[i], 0.f), 15.f) + KV_MAGIC) & 15u) << (4 * (i % 8));
         reinterpret_cast<uint2 *>(codes)[j] = make_uint2(w[0], w[1]);
         if (j % 2 == 0) reinterpret_cast<__half2 *>(par)[j / 2] = __halves2half2(s, z);
     } else {
-        float m = 0.f;
+        amax = fmaxf(amax, __shfl_xor_sync(mask, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(mask, amax, 2));
+        amax = fmaxf(amax, __shfl_xor_sync(mask, amax, 4));
+        const float s = __fdiv_rn(amax, DT == MILO_INT8 ? 127.f : 448.f);
+        float q[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
-        m = fmaxf(m, __shfl_xor_sync(mask, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(mask, m, 2));
-        m = fmaxf(m, __shfl_xor_sync(mask, m, 4));
-        const float s = __fdiv_rn(m, DT == MILO_INT8 ? 127.f : 448.f);
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        for (int i = 0; i < 16; ++i) q[i] = x[i];
+        kv_divide<16>(q, s);
+        uint32_t w[4];
+        if constexpr (DT == MILO_INT8) {
+            if (s < 0x1p-100f) {   // a scale with few bits left: 127 can be passed
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float c = s > 0.f ? __fdiv_rn(x[i], s) : 0.f;
-            uint32_t b;
-            if constexpr (DT == MILO_INT8) b = (uint32_t)(int)fminf(fmaxf(rintf(c), -127.f), 127.f) & 0xffu;
-            else b = __nv_cvt_float_to_fp8(c, __NV_SATFINITE, __NV_E4M3);
-            w[i / 4] |= b << (8 * (i % 4));
+                for (int i = 0; i < 16; ++i) q[i] = fminf(fmaxf(q[i], -127.f), 127.f);
+            }
+            kv_int8<16>(q, w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = __nv_cvt_float2_to_fp8x2(make_float2(q[4 * i], q[4 * i + 1]), __NV_SATFINITE, __NV_E4M3) |
+                       (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[4 * i + 2], q[4 * i + 3]), __NV_SATFINITE,
+                                                          __NV_E4M3) << 16;
         }
         reinterpret_cast<uint4 *>(codes)[j] = make_uint4(w[0], w[1], w[2], w[3]);
         if (j == 0) *reinterpret_cast<float *>(par) = s;
@@ -127,104 +181,184 @@ struct KvAppendArgs {
     const void *k, *v;
     int64_t sl, ss, sh, st;                  // strides of k and v in elements
     int n_new, windows;                      // blocks of block_len that a range can touch
+    int items;                               // windows * S * H * L * 2
     const int32_t *start, *count;
+};
+
+// A running channelwise minimum and maximum of 16 channels, in the elements' own type
+template <typename T> struct KvBounds;
+template <> struct KvBounds<float> {
+    float lo[16], hi[16];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            lo[i] = INFINITY;
+            hi[i] = -INFINITY;
+        }
+    }
+    __device__ __forceinline__ void add(const float (&x)[16]) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            lo[i] = fminf(lo[i], x[i]);
+            hi[i] = fmaxf(hi[i], x[i]);
+        }
+    }
+    __device__ __forceinline__ void get(float (&l)[16], float (&h)[16]) const {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            l[i] = lo[i];
+            h[i] = hi[i];
+        }
+    }
+};
+template <> struct KvBounds<__nv_bfloat16> {   // two channels an instruction
+    __nv_bfloat162 lo[8], hi[8];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            lo[i] = __float2bfloat162_rn(INFINITY);
+            hi[i] = __float2bfloat162_rn(-INFINITY);
+        }
+    }
+    __device__ __forceinline__ void add(const float (&x)[16]) {   // x are bf16 values (or +-65504, which rounds outward)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            lo[i] = __hmin2(lo[i], v);
+            hi[i] = __hmax2(hi[i], v);
+        }
+    }
+    __device__ __forceinline__ void get(float (&l)[16], float (&h)[16]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 a = __bfloat1622float2(lo[i]), b = __bfloat1622float2(hi[i]);
+            l[2 * i] = a.x;
+            l[2 * i + 1] = a.y;
+            h[2 * i] = b.x;
+            h[2 * i + 1] = b.y;
+        }
+    }
 };
 
 constexpr int KV_APPEND_WARPS = 4;
 
-// grid: windows * S * H * L * 2 CTAs (kind slowest, then layer, head, window).
-// A CTA quantises the new tokens of one block of one (layer, session, KV head)
-// and kind, four rows a warp at a time, eight lanes a row; for keys it then
-// joins the channelwise minima and maxima and writes the block's bounds.
-template <typename T, int DT>
-__global__ void __launch_bounds__(32 * KV_APPEND_WARPS) k_kv_append(KvAppendArgs a) {
-    __shared__ float s_mn[KV_APPEND_WARPS][D], s_mx[KV_APPEND_WARPS][D], s_amax[KV_APPEND_WARPS];
-    int64_t id = blockIdx.x;
-    const int win = (int)(id % a.windows);
-    id /= a.windows;
-    const int h = (int)(id % a.c.H);
-    id /= a.c.H;
-    const int s = (int)(id % a.c.S);
-    id /= a.c.S;
-    const int l = (int)(id % a.c.L), kind = (int)(id / a.c.L);
+// An item is the new tokens of one block of one (layer, session, KV head) and
+// kind (kind slowest, then layer, session, head, window).  WPI warps quantise it,
+// four rows a warp at a time, eight lanes a row with 16 channels each; for keys the
+// channelwise minima and maxima of the 4 WPI row groups are then joined in shared
+// memory, CPT channels a thread.  One token a block leaves three quarters of a
+// warp idle, so then a warp takes an item (WPI = 1); otherwise a CTA does.
+template <typename T, int DT, int WPI> __global__ void __launch_bounds__(32 * KV_APPEND_WARPS) k_kv_append(KvAppendArgs a) {
+    constexpr int CPT = D / (32 * WPI), ITEMS = KV_APPEND_WARPS / WPI;
+    __shared__ __align__(16) float s_b[ITEMS][2][4 * WPI][D];   // [item][min, max][row group][channel]
+    __shared__ float s_amax[KV_APPEND_WARPS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int wi = WPI > 1 ? warp : 0, item = WPI > 1 ? 0 : warp;   // warp of the item, item of the CTA
+    int id = blockIdx.x * ITEMS + item;
+    if (id >= a.items) return;
+    const int win = id % a.windows;
+    id /= a.windows;
+    const int h = id % a.c.H;
+    id /= a.c.H;
+    const int s = id % a.c.S;
+    id /= a.c.S;
+    const int l = id % a.c.L, kind = id / a.c.L;
     int start, n;
-    kv_range(a.start, a.count, s, a.n_new, a.c.cap, tid == 0 && h == 0 && l == 0 && win == 0 && kind == 0, start, n);
+    kv_range(a.start, a.count, s, a.n_new, a.c.cap, lane == 0 && h == 0 && l == 0 && win == 0 && kind == 0, start, n);
     const int b = start / a.c.block_len + win;
     const int t0 = max(start, b * a.c.block_len), t1 = min(start + n, (b + 1) * a.c.block_len);   // tokens written here
     if (n == 0 || t0 >= t1) return;
     const int64_t sh = (int64_t)s * a.c.H + h;
-    const T *x = (const T *)(kind ? a.v : a.k) + l * a.sl + s * a.ss + h * a.sh;
+    const int j = lane & 7, group = lane >> 3;
+    const T *x = (const T *)(kind ? a.v : a.k) + l * a.sl + s * a.ss + h * a.sh + 16 * j - start * a.st;
+    constexpr int ROW = DT == MILO_INT4 ? D / 2 : D, PAR = DT == MILO_INT4 ? 4 * KV_NG : 4;
     unsigned char *codes = a.c.codes(l, sh, kind), *par = a.c.params(l, sh, kind);
-    const int j = lane & 7;
     const unsigned mask = 0xffu << (lane & 24);
-    float mn[16], mx[16];
+    int t = t0 + 4 * wi + group;
+    KvRaw<T> next;
+    if (t < t1) next = kv_raw16<T>(x + (int64_t)t * a.st);
+    // bounds that a continued block has, of this thread's channels
+    const int64_t blk = sh * a.c.n_b + b;
+    const int ch = (32 * wi + lane) * CPT;
+    __nv_bfloat16 *held = (__nv_bfloat16 *)a.c.section(l, 4) + blk * 2 * D + ch;
+    const bool goes_on = kind == 0 && start > b * a.c.block_len;
+    float lo[CPT], hi[CPT];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        mn[i] = INFINITY;
-        mx[i] = -INFINITY;
+    for (int i = 0; i < CPT; ++i) {
+        lo[i] = goes_on ? __bfloat162float(held[i]) : INFINITY;
+        hi[i] = goes_on ? __bfloat162float(held[D + i]) : -INFINITY;
     }
+    KvBounds<T> bounds;
+    bounds.clear();
     bool bad = false;
-    for (int t = t0 + 4 * warp + (lane >> 3); t < t1; t += 4 * KV_APPEND_WARPS) {
+    for (; t < t1; t += 4 * WPI) {
         float r[16];
-        kv_load16<T>(x + (int64_t)(t - start) * a.st + 16 * j, r);
+        kv_f32<T>(next, r);
+        if (t + 4 * WPI < t1) next = kv_raw16<T>(x + (int64_t)(t + 4 * WPI) * a.st);
+        uint32_t top = 0u;                                   // greatest magnitude, by its bits
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            if (!isfinite(r[i])) {
-                bad = true;
-                r[i] = 0.f;
+        for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(r[i]) & 0x7fffffffu);
+        if (top > __float_as_uint(DT == MILO_INT4 ? KV_F16_MAX : 3.402823466e38f)) {
+            bad = true;
+            top = 0u;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (!isfinite(r[i])) r[i] = 0.f;
+                if (DT == MILO_INT4 && fabsf(r[i]) > KV_F16_MAX) r[i] = copysignf(KV_F16_MAX, r[i]);
+                top = max(top, __float_as_uint(r[i]) & 0x7fffffffu);
             }
-            if (DT == MILO_INT4 && fabsf(r[i]) > KV_F16_MAX) {
-                bad = true;
-                r[i] = copysignf(KV_F16_MAX, r[i]);
-            }
-            mn[i] = fminf(mn[i], r[i]);
-            mx[i] = fmaxf(mx[i], r[i]);
         }
-        kv_quant_store<DT>(r, j, mask, codes + (int64_t)t * a.c.row_bytes(), par + (int64_t)t * a.c.par_bytes());
+        if (kind == 0) bounds.add(r);
+        kv_quant_store<DT>(r, __uint_as_float(top), j, mask, codes + (int64_t)t * ROW, par + (int64_t)t * PAR);
     }
     if (bad) raise_status(ST_NONFINITE);
     if (kind == 1) return;
-    // channel 16 j + i over the four rows of a warp, then over the warps
+    {
+        float l16[16], h16[16];
+        bounds.get(l16, h16);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-#pragma unroll
-        for (int o = 8; o < 32; o <<= 1) {
-            mn[i] = fminf(mn[i], __shfl_xor_sync(0xffffffffu, mn[i], o));
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
-        }
-        if (lane < 8) {
-            s_mn[warp][16 * j + i] = mn[i];
-            s_mx[warp][16 * j + i] = mx[i];
+        for (int i = 0; i < 16; i += 4) {
+            *reinterpret_cast<float4 *>(&s_b[item][0][4 * wi + group][16 * j + i]) =
+                make_float4(l16[i], l16[i + 1], l16[i + 2], l16[i + 3]);
+            *reinterpret_cast<float4 *>(&s_b[item][1][4 * wi + group][16 * j + i]) =
+                make_float4(h16[i], h16[i + 1], h16[i + 2], h16[i + 3]);
         }
     }
-    __syncthreads();
-    const int64_t blk = sh * a.c.n_b + b;
-    __nv_bfloat16 *bounds = (__nv_bfloat16 *)a.c.section(l, 4) + blk * 2 * D;
-    int8_t *bcodes = (int8_t *)a.c.section(l, 5) + blk * 2 * D;
-    float lo = s_mn[0][tid], hi = s_mx[0][tid];
+    if (WPI > 1) __syncthreads();
+    else __syncwarp();
+    float m = 0.f;
 #pragma unroll
-    for (int w = 1; w < KV_APPEND_WARPS; ++w) {
-        lo = fminf(lo, s_mn[w][tid]);
-        hi = fmaxf(hi, s_mx[w][tid]);
+    for (int i = 0; i < CPT; ++i) {
+#pragma unroll
+        for (int g = 0; g < 4 * WPI; ++g) {
+            lo[i] = fminf(lo[i], s_b[item][0][g][ch + i]);
+            hi[i] = fmaxf(hi[i], s_b[item][1][g][ch + i]);
+        }
+        const __nv_bfloat16 bl = kv_outward(lo[i], false), bh = kv_outward(hi[i], true);
+        held[i] = bl;
+        held[D + i] = bh;
+        lo[i] = __bfloat162float(bl);
+        hi[i] = __bfloat162float(bh);
+        m = fmaxf(m, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
     }
-    if (start > b * a.c.block_len) {   // a block that is continued keeps what it had
-        lo = fminf(lo, __bfloat162float(bounds[tid]));
-        hi = fmaxf(hi, __bfloat162float(bounds[D + tid]));
-    }
-    const __nv_bfloat16 blo = kv_outward(lo, false), bhi = kv_outward(hi, true);
-    bounds[tid] = blo;
-    bounds[D + tid] = bhi;
-    const float flo = __bfloat162float(blo), fhi = __bfloat162float(bhi);
-    float m = fmaxf(fabsf(flo), fabsf(fhi));
+#pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) s_amax[warp] = m;
-    __syncthreads();
-    for (int w = 0; w < KV_APPEND_WARPS; ++w) m = fmaxf(m, s_amax[w]);
+    if (WPI > 1) {
+        if (lane == 0) s_amax[warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < WPI; ++w) m = fmaxf(m, s_amax[w]);
+    }
     const float sc = __fdiv_rn(m, 127.f);
-    bcodes[tid] = sc > 0.f ? (int8_t)fminf(fmaxf(rintf(__fdiv_rn(flo, sc)), -127.f), 127.f) : (int8_t)0;
-    bcodes[D + tid] = sc > 0.f ? (int8_t)fminf(fmaxf(rintf(__fdiv_rn(fhi, sc)), -127.f), 127.f) : (int8_t)0;
-    if (tid == 0) ((float *)a.c.section(l, 6))[blk] = sc;
+    int8_t *bcodes = (int8_t *)a.c.section(l, 5) + blk * 2 * D + ch;
+    kv_divide<CPT>(lo, sc);
+    kv_divide<CPT>(hi, sc);
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+        bcodes[i] = (int8_t)(int)rintf(fminf(fmaxf(lo[i], -127.f), 127.f));
+        bcodes[D + i] = (int8_t)(int)rintf(fminf(fmaxf(hi[i], -127.f), 127.f));
+    }
+    if (wi == 0 && lane == 0) ((float *)a.c.section(l, 6))[blk] = sc;
 }
 
 // the value of a lane's 16 channels (16 j ..) of one row
@@ -243,13 +377,19 @@ __device__ __forceinline__ void kv_dequant16(const unsigned char *codes, const u
         const uint4 w = __ldg(reinterpret_cast<const uint4 *>(codes) + j);
         const float s = __ldg(reinterpret_cast<const float *>(par));
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        if constexpr (DT == MILO_INT8) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint32_t c = (u[i / 4] >> (8 * (i % 4))) & 0xffu;
-            float v;
-            if constexpr (DT == MILO_INT8) v = (float)(int8_t)c;
-            else v = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3)));
-            x[i] = __fmul_rn(v, s);
+            for (int i = 0; i < 16; ++i) x[i] = __fmul_rn((float)(int8_t)(u[i / 4] >> (8 * (i % 4))), s);
+        } else {   // an e4m3's fields as an fp16's: the value times 2^-8, exactly
+            const float s8 = s * 256.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t v = __byte_perm(u[i / 2], 0u, i % 2 ? 0x3424 : 0x1404);
+                const uint32_t h = (v & 0x80008000u) | ((v >> 1) & 0x3f803f80u);
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+                x[2 * i] = __fmul_rn(f.x, s8);
+                x[2 * i + 1] = __fmul_rn(f.y, s8);
+            }
         }
     }
 }
@@ -257,32 +397,35 @@ __device__ __forceinline__ void kv_dequant16(const unsigned char *codes, const u
 struct KvReadArgs {
     KvView c;
     void *k, *v;                             // [L][S][H][n][D] or null
-    int n;
+    int n, tiles;                            // tiles of KV_READ_ROWS rows of a session's n
     const int32_t *start, *count;
-    int64_t rows;                            // L * S * H * n
 };
 
-// grid (ceil(rows * 8 / 256), 2 kinds), 256 threads: eight threads a row
+constexpr int KV_READ_ROWS = 64;
+
+// grid (L S H tiles, 2 kinds), 256 threads: eight threads a row, two rows each
 template <typename T, int DT> __global__ void __launch_bounds__(256) k_kv_read(KvReadArgs a) {
     const int kind = blockIdx.y;
     T *out = (T *)(kind ? a.v : a.k);
     if (!out) return;
-    const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, row = gid >> 3;
-    if (row >= a.rows) return;
-    const int j = (int)(gid & 7);
-    const int i = (int)(row % a.n);
-    const int64_t lsh = row / a.n;
-    const int64_t SH = (int64_t)a.c.S * a.c.H;
-    const int l = (int)(lsh / SH);
-    const int64_t sh = lsh % SH;
-    const int s = (int)(sh / a.c.H);
+    constexpr int ROW = DT == MILO_INT4 ? D / 2 : D, PAR = DT == MILO_INT4 ? 4 * KV_NG : 4;
+    const int tile = blockIdx.x % a.tiles, lsh = blockIdx.x / a.tiles;
+    const int SH = a.c.S * a.c.H, l = lsh / SH, sh = lsh % SH, s = sh / a.c.H;
+    const int tid = threadIdx.x, j = tid & 7;
     int start, n;
-    kv_range(a.start, a.count, s, a.n, a.c.cap, i == 0 && j == 0 && l == 0 && sh % a.c.H == 0, start, n);
-    if (i >= n) return;
-    const int64_t t = (int64_t)start + i;
-    float x[16];
-    kv_dequant16<DT>(a.c.codes(l, sh, kind) + t * a.c.row_bytes(), a.c.params(l, sh, kind) + t * a.c.par_bytes(), j, x);
-    kv_store16<T>(out + row * D + 16 * j, x);
+    kv_range(a.start, a.count, s, a.n, a.c.cap, tid == 0 && tile == 0 && l == 0 && sh % a.c.H == 0, start, n);
+    const unsigned char *codes = a.c.codes(l, sh, kind) + (int64_t)start * ROW;
+    const unsigned char *par = a.c.params(l, sh, kind) + (int64_t)start * PAR;
+    out += (int64_t)lsh * a.n * D + 16 * j;
+#pragma unroll
+    for (int y = 0; y < KV_READ_ROWS / 32; ++y) {
+        const int i = tile * KV_READ_ROWS + 32 * y + (tid >> 3);
+        if (i < n) {
+            float x[16];
+            kv_dequant16<DT>(codes + (int64_t)i * ROW, par + (int64_t)i * PAR, j, x);
+            kv_store16<T>(out + (int64_t)i * D, x);
+        }
+    }
 }
 
 }  // namespace milo

@@ -37,10 +37,21 @@ __device__ __forceinline__ int kv_seen(const int32_t *len, int s, int n_q, int i
     return max(0, n - n_q + i + 1);
 }
 
-constexpr int KV_SCORE_THREADS = 128, KV_SCORE_G = 8;
+constexpr int KV_SCORE_WARPS = 4, KV_SCORE_G = 8, KV_SCORE_STEP = 16 * KV_SCORE_WARPS;
 
-// grid (rows = L S n_q H, ceil(n_b / 128)): thread = block
-template <typename T> __global__ void __launch_bounds__(KV_SCORE_THREADS) k_kv_score(KvSelectArgs a) {
+__device__ __forceinline__ void kv_imma(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// grid (rows = L S n_q H, ceil(n_b / per)): a CTA scores `per` blocks of one row,
+// 16 blocks a warp at a time as the rows of m16n8k32 products of 8-bit integers,
+// the query heads its columns.  The sum's order is free: thread c of a row's four
+// reads 16-byte chunks c, c + 4, c + 8, c + 12 of a block's 256 bytes, which are the
+// operands of two steps each.  Bound by reading the codes once (260 B a block).
+template <typename T> __global__ void __launch_bounds__(32 * KV_SCORE_WARPS) k_kv_score(KvSelectArgs a, int per) {
     __shared__ __align__(16) uint32_t s_q[KV_SCORE_G][2 * D / 4];
     __shared__ float s_u[KV_SCORE_G];
     const int64_t row = blockIdx.x;
@@ -48,84 +59,110 @@ template <typename T> __global__ void __launch_bounds__(KV_SCORE_THREADS) k_kv_s
     const int64_t lsi = row / a.c.H;
     const int i = (int)(lsi % a.n_q);
     const int s = (int)((lsi / a.n_q) % a.c.S), l = (int)(lsi / a.n_q / a.c.S);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int seen = kv_seen(a.len, s, a.n_q, i, a.c.cap, tid == 0 && h == 0 && l == 0 && i == 0 && blockIdx.y == 0);
     const int cand = (seen + a.c.block_len - 1) / a.c.block_len;
-    const int b = blockIdx.y * KV_SCORE_THREADS + tid;
-    float best = -INFINITY;
+    const int b0 = blockIdx.y * per, b1 = min(a.c.n_b, b0 + per);
+    float *out = a.scores + row * a.c.n_b;
     kv_launch_next();
+    for (int b = max(b0, cand) + tid; b < b1; b += 32 * KV_SCORE_WARPS) out[b] = -INFINITY;
+    if (b0 >= cand) return;
+    const int end = min(b1, cand);
+    const int64_t base = ((int64_t)s * a.c.H + h) * a.c.n_b;
+    const unsigned char *codes = a.c.section(l, 5) + base * 2 * D + 16 * c;
+    const float *scale = reinterpret_cast<const float *>(a.c.section(l, 6)) + base;
+    uint4 w[2][4];                                  // rows g and g + 8 of the warp's 16 blocks
+    auto load = [&](int b) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                w[r][x] = make_uint4(0u, 0u, 0u, 0u);
+                if (b + g + 8 * r < end)
+                    w[r][x] = __ldg(reinterpret_cast<const uint4 *>(codes + (int64_t)(b + g + 8 * r) * 2 * D + 64 * x));
+            }
+    };
+    load(b0 + 16 * warp);
     for (int g0 = 0; g0 < a.G; g0 += KV_SCORE_G) {
         const int gn = min(KV_SCORE_G, a.G - g0);
-        __syncthreads();
-        for (int g = warp; g < gn; g += KV_SCORE_THREADS / 32) {   // lane holds channels 4 lane ..
-            const T *q = (const T *)a.q + ((lsi * a.c.H + h) * a.G + g0 + g) * D + 4 * lane;
-            float x[4], m = 0.f;
-            bool bad = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[e] = to_f32(q[e]);
-                if (!isfinite(x[e])) {
-                    bad = true;
-                    x[e] = 0.f;
-                }
-                m = fmaxf(m, fabsf(x[e]));
-            }
-            if (bad) raise_status(ST_NONFINITE);
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float u = __fdiv_rn(m, 127.f);
+        if (g0) {
+            __syncthreads();                        // the heads before these are used
+            load(b0 + 16 * warp);
+        }
+        for (int gg = warp; gg < KV_SCORE_G; gg += KV_SCORE_WARPS) {   // a head's codes; lane holds channels 4 lane ..
             uint32_t neg = 0u, pos = 0u;
+            float u = 0.f;
+            if (gg < gn) {
+                const T *q = (const T *)a.q + ((lsi * a.c.H + h) * a.G + g0 + gg) * D + 4 * lane;
+                float x[4], m = 0.f;
+                bool bad = false;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int c = u > 0.f ? (int)fminf(fmaxf(rintf(__fdiv_rn(x[e], u)), -127.f), 127.f) : 0;
-                neg |= (uint32_t)(min(c, 0) & 0xff) << (8 * e);
-                pos |= (uint32_t)(max(c, 0) & 0xff) << (8 * e);
+                for (int e = 0; e < 4; ++e) {
+                    x[e] = to_f32(q[e]);
+                    if (!isfinite(x[e])) {
+                        bad = true;
+                        x[e] = 0.f;
+                    }
+                    m = fmaxf(m, fabsf(x[e]));
+                }
+                if (bad) raise_status(ST_NONFINITE);
+                for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                u = __fdiv_rn(m, 127.f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int v = u > 0.f ? (int)fminf(fmaxf(rintf(__fdiv_rn(x[e], u)), -127.f), 127.f) : 0;
+                    neg |= (uint32_t)(min(v, 0) & 0xff) << (8 * e);
+                    pos |= (uint32_t)(max(v, 0) & 0xff) << (8 * e);
+                }
             }
-            s_q[g][lane] = neg;
-            s_q[g][32 + lane] = pos;
-            if (lane == 0) s_u[g] = u;
+            s_q[gg][lane] = neg;
+            s_q[gg][32 + lane] = pos;
+            if (lane == 0) s_u[gg] = u;
         }
         __syncthreads();
-        if (b < cand) {
-            const int64_t blk = ((int64_t)s * a.c.H + h) * a.c.n_b + b;
-            const uint4 *code = reinterpret_cast<const uint4 *>(a.c.section(l, 5) + blk * 2 * D);
-            int acc[KV_SCORE_G];
+        uint4 f[4];                                 // this thread's column of the query heads' codes
 #pragma unroll
-            for (int g = 0; g < KV_SCORE_G; ++g) acc[g] = 0;
-            for (int w = 0; w < 2 * D / 16; ++w) {
-                const uint4 u = __ldg(code + w);
+        for (int x = 0; x < 4; ++x) f[x] = *reinterpret_cast<const uint4 *>(&s_q[g][4 * c + 16 * x]);
+        const float u0 = s_u[2 * c], u1 = s_u[2 * c + 1];
+        for (int b = b0 + 16 * warp; b < end; b += KV_SCORE_STEP) {
+            int acc[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int g = 0; g < KV_SCORE_G; ++g) {
-                    if (g >= gn) break;
-                    const uint4 c = reinterpret_cast<const uint4 *>(s_q[g])[w];
-                    acc[g] = __dp4a((int)u.x, (int)c.x, acc[g]);
-                    acc[g] = __dp4a((int)u.y, (int)c.y, acc[g]);
-                    acc[g] = __dp4a((int)u.z, (int)c.z, acc[g]);
-                    acc[g] = __dp4a((int)u.w, (int)c.w, acc[g]);
+            for (int x = 0; x < 4; ++x) {
+                kv_imma(acc, w[0][x].x, w[1][x].x, w[0][x].y, w[1][x].y, f[x].x, f[x].y);
+                kv_imma(acc, w[0][x].z, w[1][x].z, w[0][x].w, w[1][x].w, f[x].z, f[x].w);
+            }
+            load(b + KV_SCORE_STEP);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float v = 2 * c < gn ? __fmul_rn((float)acc[2 * r], u0) : -INFINITY;
+                if (2 * c + 1 < gn) v = fmaxf(v, __fmul_rn((float)acc[2 * r + 1], u1));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+                const int at = b + g + 8 * r;
+                if (c == 0 && at < end) {
+                    if (g0) v = fmaxf(v, out[at]);  // the heads before; the scale comes with the last ones
+                    out[at] = g0 + KV_SCORE_G >= a.G ? __fmul_rn(v, __ldg(scale + at)) : v;
                 }
             }
-#pragma unroll
-            for (int g = 0; g < KV_SCORE_G; ++g)
-                if (g < gn) best = fmaxf(best, __fmul_rn((float)acc[g], s_u[g]));
-            if (g0 + KV_SCORE_G >= a.G) best = __fmul_rn(best, __ldg((const float *)a.c.section(l, 6) + blk));
         }
     }
-    if (b < a.c.n_b) a.scores[row * a.c.n_b + b] = best;
 }
 
-// larger float = larger key; forced candidates above all
-__device__ __forceinline__ uint32_t kv_key(float x, bool forced) {
-    if (forced) return 0xffffffffu;
+// larger float = larger key, 1 at least and below 2^32 - 1 (only NaN would be either)
+__device__ __forceinline__ uint32_t kv_key(float x) {
     if (x == 0.f) x = 0.f;   // -0 ties with +0
     const uint32_t b = __float_as_uint(x);
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+    return min(max(b & 0x80000000u ? ~b : b | 0x80000000u, 1u), 0xfffffffeu);
 }
 
-constexpr int KV_TOPN_THREADS = 256;
-
-// one CTA per row: the n_sel-th greatest key by four 8-bit histogram passes,
-// then the ids above it and the first of those equal to it, in order
-__global__ void __launch_bounds__(KV_TOPN_THREADS) k_kv_topn(KvSelectArgs a) {
-    __shared__ int s_hist[256], s_gt[KV_TOPN_THREADS / 32], s_eq[KV_TOPN_THREADS / 32], s_bin, s_above;
+// One CTA per row.  The n_sel-th greatest key is found two bits at a time: a
+// round counts the keys at or above three thresholds.  A thread keeps KEYS
+// consecutive keys in registers, so that ids come out in order after one scan;
+// HELD = false reads them from the scores again in every round (more blocks than
+// THREADS * KEYS).
+template <int THREADS, int KEYS, bool HELD> __global__ void __launch_bounds__(THREADS) k_kv_topn(KvSelectArgs a) {
+    constexpr int WARPS = THREADS / 32;
+    __shared__ int s_n[2][WARPS][4];
     kv_wait_previous();
     const int64_t row = blockIdx.x;
     const int64_t lsi = row / a.c.H;
@@ -136,57 +173,124 @@ __global__ void __launch_bounds__(KV_TOPN_THREADS) k_kv_topn(KvSelectArgs a) {
     const float *sc = a.scores + row * a.c.n_b;
     int32_t *out = a.selected + row * a.n_sel;
     if (cand <= a.n_sel) {
-        for (int e = tid; e < a.n_sel; e += KV_TOPN_THREADS) out[e] = e < cand ? e : -1;
+        for (int e = tid; e < a.n_sel; e += THREADS) out[e] = e < cand ? e : -1;
         return;
     }
-    const int last = cand - a.n_last;
-    uint32_t prefix = 0u, mask = 0u;
-    int want = a.n_sel;                     // how many of the keys that match the prefix are taken
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int e = tid; e < 256; e += KV_TOPN_THREADS) s_hist[e] = 0;
-        __syncthreads();
-        for (int b = tid; b < cand; b += KV_TOPN_THREADS) {
-            const uint32_t k = kv_key(sc[b], b < a.n_first || b >= last);
-            if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & 255u], 1);
-        }
-        __syncthreads();
-        if (tid == 0) {
-            int above = 0, bin = 255;
-            while (above + s_hist[bin] < want) above += s_hist[bin--];
-            s_bin = bin;
-            s_above = above;
-        }
-        __syncthreads();
-        prefix |= (uint32_t)s_bin << shift;
-        mask |= 255u << shift;
-        want -= s_above;
-        __syncthreads();
+    const int last = cand - a.n_last, n_sel = a.n_sel - a.n_first - a.n_last;   // to be found beside the forced ones
+    const int mine = HELD ? KEYS : (cand + THREADS - 1) / THREADS;   // ids tid * mine ..
+    const int first = tid * mine;
+    auto forced = [&](int b) { return b < a.n_first || (b >= last && b < cand); };
+    auto key_of = [&](int b) { return b < cand && !forced(b) ? kv_key(sc[b]) : 0u; };
+    uint32_t key[KEYS];
+#pragma unroll
+    for (int x = 0; x < KEYS; ++x) key[x] = HELD ? key_of(first + x) : 0u;
+    // greatest threshold t with at least n_sel keys >= t (a key is 0 only where there is no candidate to be found): the
+    // bits that all keys share come from their least and greatest
+    uint32_t lo = 0xffffffffu, hi = 0u;
+    auto range = [&](uint32_t k) {
+        hi = max(hi, k);
+        lo = min(lo, k - 1u);                        // 0 wraps: not a key
+    };
+    if (HELD) {
+#pragma unroll
+        for (int x = 0; x < KEYS; ++x) range(key[x]);
+    } else {
+        for (int b = tid; b < cand; b += THREADS) range(key_of(b));
     }
-    int gt0 = 0, eq0 = 0;                   // ids above / equal before this round of blocks
-    for (int b0 = 0; b0 < cand; b0 += KV_TOPN_THREADS) {
-        const int b = b0 + tid;
-        const uint32_t k = b < cand ? kv_key(sc[b], b < a.n_first || b >= last) : 0u;
-        const bool gt = b < cand && k > prefix, eq = b < cand && k == prefix;
-        const unsigned mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-        if (lane == 0) {
-            s_gt[warp] = __popc(mg);
-            s_eq[warp] = __popc(me);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    if (lane == 0) *reinterpret_cast<uint2 *>(s_n[1][warp]) = make_uint2(lo, hi);
+    __syncthreads();
+    {
+        const uint2 v = *reinterpret_cast<const uint2 *>(s_n[1][lane % WARPS]);
+        lo = __reduce_min_sync(0xffffffffu, v.x) + 1u;
+        hi = __reduce_max_sync(0xffffffffu, v.y);
+    }
+    const uint32_t differ = lo ^ hi;
+    int shift = differ ? (31 - __clz(differ)) & ~1 : -2;
+    uint32_t t = n_sel == 0 ? 0xffffffffu : shift >= 30 ? 0u : hi & ~((4u << max(shift, 0)) - 1u);
+    if (differ == 0u) t = n_sel == 0 ? 0xffffffffu : hi;
+    if (n_sel == 0) shift = -2;
+    // the first round uses the other buffer than the range did
+    for (int round = 0; shift >= 0; shift -= 2, ++round) {
+        const uint32_t t1 = t | (1u << shift), t2 = t | (2u << shift), t3 = t | (3u << shift);
+        int n1 = 0, n2 = 0, n3 = 0;
+        auto count = [&](uint32_t k) {
+            n1 += k >= t1;
+            n2 += k >= t2;
+            n3 += k >= t3;
+        };
+        if (HELD) {
+#pragma unroll
+            for (int x = 0; x < KEYS; ++x) count(key[x]);
+        } else {
+            for (int b = tid; b < cand; b += THREADS) count(key_of(b));
         }
+        n1 = __reduce_add_sync(0xffffffffu, n1);
+        n2 = __reduce_add_sync(0xffffffffu, n2);
+        n3 = __reduce_add_sync(0xffffffffu, n3);
+        const int buf = round & 1;                   // two buffers: one barrier a round
+        if (lane == 0) *reinterpret_cast<int4 *>(s_n[buf][warp]) = make_int4(n1, n2, n3, 0);
         __syncthreads();
-        int g = gt0, e = eq0;
-        for (int w = 0; w < KV_TOPN_THREADS / 32; ++w) {
-            if (w < warp) {
-                g += s_gt[w];
-                e += s_eq[w];
-            }
-            gt0 += s_gt[w];
-            eq0 += s_eq[w];
+        const int4 v = *reinterpret_cast<const int4 *>(s_n[buf][lane % WARPS]);   // each warp adds the warps' counts
+        const bool own = lane < WARPS;
+        n1 = __reduce_add_sync(0xffffffffu, own ? v.x : 0);
+        n2 = __reduce_add_sync(0xffffffffu, own ? v.y : 0);
+        n3 = __reduce_add_sync(0xffffffffu, own ? v.z : 0);
+        const int n = n3 >= n_sel ? n3 : n2 >= n_sel ? n2 : n1;
+        t = n3 >= n_sel ? t3 : n2 >= n_sel ? t2 : n1 >= n_sel ? t1 : t;
+        if (n == n_sel) {                            // exactly the keys >= t: all above t - 1
+            --t;
+            break;
         }
-        const unsigned below = (1u << lane) - 1u;
-        g += __popc(mg & below);
-        e += __popc(me & below);
-        if (gt || (eq && e < want)) out[g + min(e, want)] = b;
-        __syncthreads();
+    }
+    // keys above t are all taken, and the first of those equal to it
+    int gt = 0, eq = 0;
+    auto tally = [&](uint32_t k, int b) {
+        gt += k > t || forced(b);
+        eq += k == t && k != 0u;
+    };
+    if (HELD) {
+#pragma unroll
+        for (int x = 0; x < KEYS; ++x) tally(key[x], first + x);
+    } else {
+        for (int x = 0; x < mine; ++x) tally(key_of(first + x), first + x);
+    }
+    int ig = gt, ie = eq;                            // inclusive over the threads
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, ig, o), y = __shfl_up_sync(0xffffffffu, ie, o);
+        if (lane >= o) {
+            ig += x;
+            ie += y;
+        }
+    }
+    __syncthreads();
+    if (lane == 31) *reinterpret_cast<int2 *>(s_n[0][warp]) = make_int2(ig, ie);
+    __syncthreads();
+    int all = 0;
+    ig -= gt;
+    ie -= eq;
+    for (int w = 0; w < WARPS; ++w) {
+        const int2 v = *reinterpret_cast<const int2 *>(s_n[0][w]);
+        if (w < warp) {
+            ig += v.x;
+            ie += v.y;
+        }
+        all += v.x;
+    }
+    const int want = a.n_sel - all;                  // how many of the equal ones
+    auto put = [&](uint32_t k, int b) {
+        const bool g = k > t || forced(b), e = k == t && k != 0u;
+        if (g) out[ig + min(ie, want)] = b;
+        else if (e && ie < want) out[ig + ie] = b;
+        ig += g;
+        ie += e;
+    };
+    if (HELD) {
+#pragma unroll
+        for (int x = 0; x < KEYS; ++x) put(key[x], first + x);
+    } else {
+        for (int x = 0; x < mine; ++x) put(key_of(first + x), first + x);
     }
 }
 

@@ -29,25 +29,36 @@ struct RopeArgs {
     float sgn;                           // -1: transposed
 };
 
-template <typename T, int V> __device__ __forceinline__ void rope_load(const T *p, float (&v)[V]) {
-    constexpr int B = V * (int)sizeof(T);
-    if constexpr (B % 16 == 0) {
-        uint4 w[B / 16];
+// V elements as they lie, and as fp32
+template <typename T, int V> struct RopeRaw {
+    static constexpr int B = V * (int)sizeof(T);
+    static constexpr bool VEC = B % 16 == 0, HALF16 = B == 8 && V >= 4;
+    uint4 w[VEC ? B / 16 : 1];
+    T e[VEC || HALF16 ? 1 : V];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < B / 16; ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
-        const T *e = reinterpret_cast<const T *>(w);
+            for (int i = 0; i < B / 16; ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
+        } else if constexpr (HALF16) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            w[0].x = u.x;
+            w[0].y = u.y;
+        } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = to_f32(e[i]);
-    } else if constexpr (B == 8 && V >= 4) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(p);
-        const T *e = reinterpret_cast<const T *>(&w);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = to_f32(e[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = to_f32(p[i]);
+            for (int i = 0; i < V; ++i) e[i] = p[i];
+        }
     }
-}
+    __device__ __forceinline__ void get(float (&v)[V]) const {
+        if constexpr (VEC || HALF16) {
+            const T *t = reinterpret_cast<const T *>(w);
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = to_f32(t[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[i] = to_f32(e[i]);
+        }
+    }
+};
 
 template <typename T, int V> __device__ __forceinline__ void rope_store(T *p, const float (&v)[V]) {
     constexpr int B = V * (int)sizeof(T);
@@ -73,7 +84,7 @@ template <typename T, int V> __device__ __forceinline__ void rope_store(T *p, co
 // V elements per access.  INTER: a unit is V neighbouring channels (V / 2
 // pairs); otherwise V pairs (i, i + rd / 2), i.e. two accesses.
 template <typename TX, typename TY, int V, bool INTER>
-__global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(256, 3) k_rope(const __grid_constant__ RopeArgs a) {
     const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int u = (int)(gid % a.units);
     const int64_t r = gid / a.units;
@@ -86,13 +97,17 @@ __global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeArgs a
     if (u >= a.rot_units) {   // channels that do not turn
         const int c = a.rd + (u - a.rot_units) * V;
         for (int h = h0; h < h1; ++h) {
+            RopeRaw<TX, V> r;
             float v[V];
-            rope_load<TX, V>(x + h * a.xh + c, v);
+            r.load(x + h * a.xh + c);
+            r.get(v);
             rope_store<TY, V>(y + h * a.yh + c, v);
         }
         return;
     }
     constexpr int NP = INTER ? (V + 1) / 2 : V;   // pairs of a unit
+    // heads whose loads are issued together: up to 128 bytes in flight a thread
+    constexpr int FIT = 128 / (V * (int)sizeof(TX) * (INTER ? 1 : 2)), ROPE_HEADS = FIT < 4 ? FIT : 4;
     const double p = (double)a.pos[t % a.n_pos];
     float cs[NP], sn[NP];
     const int i0 = u * NP;
@@ -106,29 +121,48 @@ __global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeArgs a
     }
     if constexpr (INTER) {
         static_assert(V % 2 == 0, "a unit of neighbouring channels holds whole pairs");
-        for (int h = h0; h < h1; ++h) {
-            float v[V], w[V];
-            rope_load<TX, V>(x + h * a.xh + u * V, v);
+        for (int h = h0; h < h1; h += ROPE_HEADS) {
+            RopeRaw<TX, V> r[ROPE_HEADS];
 #pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                w[2 * i] = v[2 * i] * cs[i] - v[2 * i + 1] * sn[i];
-                w[2 * i + 1] = v[2 * i] * sn[i] + v[2 * i + 1] * cs[i];
+            for (int e = 0; e < ROPE_HEADS; ++e)
+                if (h + e < h1) r[e].load(x + (h + e) * a.xh + u * V);
+#pragma unroll
+            for (int e = 0; e < ROPE_HEADS; ++e) {
+                float v[V], w[V];
+                r[e].get(v);
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    w[2 * i] = v[2 * i] * cs[i] - v[2 * i + 1] * sn[i];
+                    w[2 * i + 1] = v[2 * i] * sn[i] + v[2 * i + 1] * cs[i];
+                }
+                if (h + e < h1) rope_store<TY, V>(y + (h + e) * a.yh + u * V, w);
             }
-            rope_store<TY, V>(y + h * a.yh + u * V, w);
         }
     } else {
         const int c0 = u * V, c1 = a.rd / 2 + u * V;
-        for (int h = h0; h < h1; ++h) {
-            float v[V], w[V], p0[V], p1[V];
-            rope_load<TX, V>(x + h * a.xh + c0, v);
-            rope_load<TX, V>(x + h * a.xh + c1, w);
+        for (int h = h0; h < h1; h += ROPE_HEADS) {
+            RopeRaw<TX, V> r0[ROPE_HEADS], r1[ROPE_HEADS];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                p0[i] = v[i] * cs[i] - w[i] * sn[i];
-                p1[i] = v[i] * sn[i] + w[i] * cs[i];
+            for (int e = 0; e < ROPE_HEADS; ++e)
+                if (h + e < h1) {
+                    r0[e].load(x + (h + e) * a.xh + c0);
+                    r1[e].load(x + (h + e) * a.xh + c1);
+                }
+#pragma unroll
+            for (int e = 0; e < ROPE_HEADS; ++e) {
+                float v[V], w[V], p0[V], p1[V];
+                r0[e].get(v);
+                r1[e].get(w);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    p0[i] = v[i] * cs[i] - w[i] * sn[i];
+                    p1[i] = v[i] * sn[i] + w[i] * cs[i];
+                }
+                if (h + e < h1) {
+                    rope_store<TY, V>(y + (h + e) * a.yh + c0, p0);
+                    rope_store<TY, V>(y + (h + e) * a.yh + c1, p1);
+                }
             }
-            rope_store<TY, V>(y + h * a.yh + c0, p0);
-            rope_store<TY, V>(y + h * a.yh + c1, p1);
         }
     }
 }

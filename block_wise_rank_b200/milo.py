@@ -490,13 +490,14 @@ def milo_rope_freqs(params: milo_rope_params):
     return list(w)[:(params.rotary_dim or params.d) // 2], m.value
 
 
-def _on(t: torch.Tensor, stream):
-    """The stream of a call on t, which lives on the current CUDA device."""
+def _on(t: torch.Tensor, stream) -> int:
+    """The raw stream of a call on t, which lives on the current CUDA device."""
     if not t.is_cuda:
         raise ValueError(f"tensor on {t.device}, a CUDA tensor expected")
-    if t.device.index != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"tensor on {t.device}, and the current device is cuda:{torch.cuda.current_device()}")
-    return ctypes.c_void_p((stream or torch.cuda.current_stream()).cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _used_on(stream, *tensors):
@@ -507,14 +508,15 @@ def _used_on(stream, *tensors):
                 t.record_stream(stream)
 
 
-def _same_device(device, *tensors):
+def _same_device(first, *tensors):
+    dev = first.get_device()
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
 
 
 def _int32(t: torch.Tensor, shape, what: str):
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what}: contiguous int32 {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
 
 
@@ -531,11 +533,13 @@ def milo_rope(x: torch.Tensor, positions: torch.Tensor, params: milo_rope_params
         out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
     elif out.shape != x.shape or (out.numel() and out.stride(2) != 1):
         raise ValueError(f"out: {tuple(x.shape)} with contiguous rows expected, got {tuple(out.shape)}")
-    _int32(positions, (positions.numel(),), "positions")
-    _same_device(x.device, out, positions)
-    rc = lib().milo_rope(params, x.data_ptr(), _dtype_code(x.dtype), x.stride(0), x.stride(1), out.data_ptr(),
-                         _dtype_code(out.dtype), out.stride(0), out.stride(1), positions.data_ptr(),
-                         positions.numel(), x.shape[0], x.shape[1], int(transpose), s)
+    n_pos = positions.numel()
+    _int32(positions, (n_pos,), "positions")
+    _same_device(x, out, positions)
+    n, h, _ = x.shape
+    xs, ys = x.stride(), out.stride()
+    rc = lib().milo_rope(params, x.data_ptr(), _dtype_code(x.dtype), xs[0], xs[1], out.data_ptr(),
+                         _dtype_code(out.dtype), ys[0], ys[1], positions.data_ptr(), n_pos, n, h, transpose, s)
     _used_on(stream, out)
     _check(rc, "milo_rope")
     return out
@@ -569,6 +573,13 @@ class KvCache:
         self.buf = _bytes(n, device) if buf is None else buf
         if self.buf.dtype != torch.uint8 or not self.buf.is_contiguous():
             raise ValueError("a cache's buffer is a contiguous uint8 tensor")
+        self._sizes = {}   # workspace bytes by call shape
+
+    def _ws(self, name: str, *args) -> int:
+        n = self._sizes.get((name, args))
+        if n is None:
+            n = self._sizes[name, args] = getattr(lib(), name)(ctypes.byref(self.shape), *args)
+        return n
 
     @property
     def n_b(self) -> int:
@@ -600,7 +611,7 @@ def milo_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, start: torc
     _int32(start, (c.S,), "start")
     if count is not None:
         _int32(count, (c.S,), "count")
-    _same_device(k.device, v, start, count, cache.buf)
+    _same_device(k, v, start, count, cache.buf)
     strides = None if k.is_contiguous() else (ctypes.c_int64 * 4)(*st[:4])
     rc = lib().milo_kv_append(c, cache.buf.data_ptr(), cache.buf.numel(), k.data_ptr(), v.data_ptr(),
                               _dtype_code(k.dtype), strides, k.shape[3], start.data_ptr(),
@@ -625,7 +636,7 @@ def milo_kv_read(cache: KvCache, start: torch.Tensor, n: int, count=None, k_out=
     _int32(start, (c.S,), "start")
     if count is not None:
         _int32(count, (c.S,), "count")
-    _same_device(k_out.device, v_out, start, count, cache.buf)
+    _same_device(k_out, v_out, start, count, cache.buf)
     rc = lib().milo_kv_read(c, cache.buf.data_ptr(), cache.buf.numel(), n, start.data_ptr(),
                             None if count is None else count.data_ptr(), k_out.data_ptr(), v_out.data_ptr(),
                             _dtype_code(k_out.dtype), s)
@@ -637,10 +648,11 @@ def milo_kv_read(cache: KvCache, start: torch.Tensor, n: int, count=None, k_out=
 def _kv_queries(cache: KvCache, q: torch.Tensor, length: torch.Tensor):
     """(n_q, Hq) of q [L][S][n_q][Hq][d] or [L][S][Hq][d]."""
     c = cache.shape
-    if q.dim() not in (4, 5) or tuple(q.shape[:2]) != (c.L, c.S) or q.shape[-1] != c.d or not q.is_contiguous():
-        raise ValueError(f"q: contiguous [{c.L}][{c.S}]([n_q])[Hq][{c.d}] expected, got {tuple(q.shape)}")
+    shape = q.shape
+    if len(shape) not in (4, 5) or shape[0] != c.L or shape[1] != c.S or shape[-1] != c.d or not q.is_contiguous():
+        raise ValueError(f"q: contiguous [{c.L}][{c.S}]([n_q])[Hq][{c.d}] expected, got {tuple(shape)}")
     _int32(length, (c.S,), "length")
-    return (q.shape[2] if q.dim() == 5 else 1), q.shape[-2]
+    return (shape[2] if len(shape) == 5 else 1), shape[-2]
 
 
 def milo_kv_select(cache: KvCache, q: torch.Tensor, length: torch.Tensor, n_sel: int, n_first: int = 0,
@@ -662,8 +674,8 @@ def milo_kv_select(cache: KvCache, q: torch.Tensor, length: torch.Tensor, n_sel:
                                not scores.is_contiguous()):
         raise ValueError(f"scores: contiguous float32 {lead + (cache.n_b,)} expected")
     if workspace is None:
-        workspace = _bytes(lib().milo_kv_select_workspace_size(c, n_q), q.device)
-    _same_device(q.device, length, selected, scores, workspace, cache.buf)
+        workspace = _bytes(cache._ws("milo_kv_select_workspace_size", n_q), q.device)
+    _same_device(q, length, selected, scores, workspace, cache.buf)
     rc = lib().milo_kv_select(c, cache.buf.data_ptr(), cache.buf.numel(), q.data_ptr(), _dtype_code(q.dtype), n_q, Hq,
                               length.data_ptr(), n_sel, n_first, n_last, selected.data_ptr(),
                               None if scores is None else scores.data_ptr(), workspace.data_ptr(), workspace.numel(),
@@ -695,8 +707,8 @@ def milo_kv_attn(cache: KvCache, q: torch.Tensor, length: torch.Tensor, selected
         raise ValueError("out: like q expected")
     lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if return_lse else None
     if workspace is None:
-        workspace = _bytes(lib().milo_kv_attn_workspace_size(c, n_q, Hq, n_sel), q.device)
-    _same_device(q.device, length, selected, out, workspace, cache.buf)
+        workspace = _bytes(cache._ws("milo_kv_attn_workspace_size", n_q, Hq, n_sel), q.device)
+    _same_device(q, length, selected, out, workspace, cache.buf)
     rc = lib().milo_kv_attn(c, cache.buf.data_ptr(), cache.buf.numel(), q.data_ptr(), _dtype_code(q.dtype), n_q, Hq,
                             length.data_ptr(), None if selected is None else selected.data_ptr(), n_sel, scale,
                             out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
@@ -730,7 +742,7 @@ def milo_decode_attn_kv(f: Factors, q: torch.Tensor, selected: torch.Tensor, cac
     n_sel = selected.shape[-1]
     if workspace is None:
         workspace = _bytes(lib().milo_decode_kv_workspace_size(f.handle, c.S, Hq, n_sel, c, kv_n_sel), q.device)
-    _same_device(q.device, length, selected, positions, kv_selected, out, workspace, cache.buf)
+    _same_device(q, length, selected, positions, kv_selected, out, workspace, cache.buf)
     rc = lib().milo_decode_attn_kv(f.handle, q.data_ptr(), c.S, Hq, selected.data_ptr(),
                                    None if positions is None else positions.data_ptr(), n_sel, float(rope_base), c,
                                    cache.buf.data_ptr(), cache.buf.numel(), length.data_ptr(),
