@@ -120,8 +120,9 @@ milo_status kv_query_check(const milo_kv_shape *s, const void *q, milo_dtype q_d
 unsigned grid_x(int64_t ctas) { return ctas > INT32_MAX ? 0u : (unsigned)ctas; }
 
 template <typename T, int DT> void kv_append_run(const KvAppendArgs &a, cudaStream_t s) {
-    // up to four tokens are one step of a warp: a warp takes an item (28 layers x 8 sessions x 4 heads, one token)
-    if (a.n_new <= 4)
+    // a warp to an item where a step takes all its tokens, or where the items fill the GPU (16 warps an SM) twice over:
+    // what an item costs beside its rows is then paid once a warp, not by four
+    if (a.n_new <= 4 || a.items >= 32 * sm_count())
         k_kv_append<T, DT, 1><<<(a.items + KV_APPEND_WARPS - 1) / KV_APPEND_WARPS, 32 * KV_APPEND_WARPS, 0, s>>>(a);
     else
         k_kv_append<T, DT, KV_APPEND_WARPS><<<a.items, 32 * KV_APPEND_WARPS, 0, s>>>(a);

@@ -55,6 +55,20 @@ template <typename T> __device__ __forceinline__ KvRaw<T> kv_raw16(const T *p) {
     for (int i = 0; i < (int)sizeof(T); ++i) r.w[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
     return r;
 }
+// the bits of the greatest magnitude, as an fp32's (above 0x7f7fffff: not finite)
+template <typename T> __device__ __forceinline__ uint32_t kv_top(const KvRaw<T> &r) {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(r.w);
+    uint32_t top = 0u;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = max(top, w[i] & 0x7fffffffu);
+        return top;
+    } else {   // two values an instruction
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+        return max(top & 0xffff0000u, top << 16);
+    }
+}
 template <typename T> __device__ __forceinline__ void kv_f32(const KvRaw<T> &r, float (&x)[16]) {
     const uint32_t *w = reinterpret_cast<const uint32_t *>(r.w);
 #pragma unroll
@@ -62,19 +76,6 @@ template <typename T> __device__ __forceinline__ void kv_f32(const KvRaw<T> &r, 
         if constexpr (sizeof(T) == 4) x[i] = __uint_as_float(w[i]);
         else x[i] = __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
     }
-}
-
-template <typename T> __device__ __forceinline__ void kv_store16(T *p, const float (&x)[16]) {
-    constexpr int N = (int)sizeof(T);
-    uint4 w[N];
-    T *e = reinterpret_cast<T *>(w);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        if constexpr (sizeof(T) == 4) e[i] = x[i];
-        else e[i] = __float2bfloat16_rn(x[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) reinterpret_cast<uint4 *>(p)[i] = w[i];
 }
 
 // x / s rounded like an IEEE division, from inv = 1 / s rounded: by Markstein
@@ -89,6 +90,10 @@ __device__ __forceinline__ float kv_quotient(float x, float s, float inv) {
     return fmaf(fmaf(-q, s, x), inv, q);
 }
 __device__ __forceinline__ bool kv_plain_scale(float s) { return s > 0x1p-60f && s < 0x1p100f; }
+// x / n for a constant n
+template <int N> __device__ __forceinline__ float kv_over(float x) {
+    return x > 0x1p-60f ? kv_quotient(x, (float)N, 1.f / (float)N) : __fdiv_rn(x, (float)N);
+}
 // x[i] / s for every i; 0 where s is 0
 template <int N> __device__ __forceinline__ void kv_divide(float (&x)[N], float s) {
     if (kv_plain_scale(s)) {
@@ -116,10 +121,11 @@ template <int N> __device__ __forceinline__ void kv_int8(const float (&q)[N], ui
 }
 
 // Quantise a lane's 16 channels (lane j of 8 holds channels 16 j ..) of one row
-// and store its codes and parameters.  All 8 lanes of the row call it together.
+// and store its codes and parameters where the row is `live`.  The whole warp calls it together.
 template <int DT>
-__device__ __forceinline__ void kv_quant_store(const float (&x)[16], float amax, int j, unsigned mask,
+__device__ __forceinline__ void kv_quant_store(const float (&x)[16], float amax, int j, bool live,
                                                unsigned char *codes, unsigned char *par) {
+    constexpr unsigned mask = 0xffffffffu;
     if constexpr (DT == MILO_INT4) {
         float lo = x[0], hi = x[0];
 #pragma unroll
@@ -139,13 +145,13 @@ __device__ __forceinline__ void kv_quant_store(const float (&x)[16], float amax,
 #pragma unroll
         for (int i = 0; i < 16; ++i)   // clamped before it is rounded: the same code, and within the trick's range
             w[i / 8] |= (__float_as_uint(fminf(fmaxf(q[i], 0.f), 15.f) + KV_MAGIC) & 15u) << (4 * (i % 8));
-        reinterpret_cast<uint2 *>(codes)[j] = make_uint2(w[0], w[1]);
-        if (j % 2 == 0) reinterpret_cast<__half2 *>(par)[j / 2] = __halves2half2(s, z);
+        if (live) reinterpret_cast<uint2 *>(codes)[j] = make_uint2(w[0], w[1]);
+        if (live && j % 2 == 0) reinterpret_cast<__half2 *>(par)[j / 2] = __halves2half2(s, z);
     } else {
         amax = fmaxf(amax, __shfl_xor_sync(mask, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(mask, amax, 2));
         amax = fmaxf(amax, __shfl_xor_sync(mask, amax, 4));
-        const float s = __fdiv_rn(amax, DT == MILO_INT8 ? 127.f : 448.f);
+        const float s = kv_over<DT == MILO_INT8 ? 127 : 448>(amax);
         float q[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) q[i] = x[i];
@@ -164,8 +170,8 @@ __device__ __forceinline__ void kv_quant_store(const float (&x)[16], float amax,
                        (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[4 * i + 2], q[4 * i + 3]), __NV_SATFINITE,
                                                           __NV_E4M3) << 16;
         }
-        reinterpret_cast<uint4 *>(codes)[j] = make_uint4(w[0], w[1], w[2], w[3]);
-        if (j == 0) *reinterpret_cast<float *>(par) = s;
+        if (live) reinterpret_cast<uint4 *>(codes)[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        if (live && j == 0) *reinterpret_cast<float *>(par) = s;
     }
 }
 
@@ -196,6 +202,7 @@ template <> struct KvBounds<float> {
             hi[i] = -INFINITY;
         }
     }
+    __device__ __forceinline__ void add(const KvRaw<float> &, const float (&x)[16]) { add(x); }
     __device__ __forceinline__ void add(const float (&x)[16]) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -218,6 +225,14 @@ template <> struct KvBounds<__nv_bfloat16> {   // two channels an instruction
         for (int i = 0; i < 8; ++i) {
             lo[i] = __float2bfloat162_rn(INFINITY);
             hi[i] = __float2bfloat162_rn(-INFINITY);
+        }
+    }
+    __device__ __forceinline__ void add(const KvRaw<__nv_bfloat16> &r, const float (&)[16]) {
+        const __nv_bfloat162 *v = reinterpret_cast<const __nv_bfloat162 *>(r.w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            lo[i] = __hmin2(lo[i], v[i]);
+            hi[i] = __hmax2(hi[i], v[i]);
         }
     }
     __device__ __forceinline__ void add(const float (&x)[16]) {   // x are bf16 values (or +-65504, which rounds outward)
@@ -248,7 +263,8 @@ constexpr int KV_APPEND_WARPS = 4;
 // channelwise minima and maxima of the 4 WPI row groups are then joined in shared
 // memory, CPT channels a thread.  One token a block leaves three quarters of a
 // warp idle, so then a warp takes an item (WPI = 1); otherwise a CTA does.
-template <typename T, int DT, int WPI> __global__ void __launch_bounds__(32 * KV_APPEND_WARPS) k_kv_append(KvAppendArgs a) {
+template <typename T, int DT, int WPI>
+__global__ void __launch_bounds__(32 * KV_APPEND_WARPS, sizeof(T) == 4 ? 5 : 6) k_kv_append(KvAppendArgs a) {
     constexpr int CPT = D / (32 * WPI), ITEMS = KV_APPEND_WARPS / WPI;
     __shared__ __align__(16) float s_b[ITEMS][2][4 * WPI][D];   // [item][min, max][row group][channel]
     __shared__ float s_amax[KV_APPEND_WARPS];
@@ -273,9 +289,8 @@ template <typename T, int DT, int WPI> __global__ void __launch_bounds__(32 * KV
     const T *x = (const T *)(kind ? a.v : a.k) + l * a.sl + s * a.ss + h * a.sh + 16 * j - start * a.st;
     constexpr int ROW = DT == MILO_INT4 ? D / 2 : D, PAR = DT == MILO_INT4 ? 4 * KV_NG : 4;
     unsigned char *codes = a.c.codes(l, sh, kind), *par = a.c.params(l, sh, kind);
-    const unsigned mask = 0xffu << (lane & 24);
     int t = t0 + 4 * wi + group;
-    KvRaw<T> next;
+    KvRaw<T> next{};
     if (t < t1) next = kv_raw16<T>(x + (int64_t)t * a.st);
     // bounds that a continued block has, of this thread's channels
     const int64_t blk = sh * a.c.n_b + b;
@@ -291,14 +306,14 @@ template <typename T, int DT, int WPI> __global__ void __launch_bounds__(32 * KV
     KvBounds<T> bounds;
     bounds.clear();
     bool bad = false;
-    for (; t < t1; t += 4 * WPI) {
+    for (; t - group < t1; t += 4 * WPI) {                   // the whole warp, rows behind the last with what was there
+        const bool live = t < t1;
+        const KvRaw<T> raw = next;
         float r[16];
-        kv_f32<T>(next, r);
+        kv_f32<T>(raw, r);
         if (t + 4 * WPI < t1) next = kv_raw16<T>(x + (int64_t)(t + 4 * WPI) * a.st);
-        uint32_t top = 0u;                                   // greatest magnitude, by its bits
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(r[i]) & 0x7fffffffu);
-        if (top > __float_as_uint(DT == MILO_INT4 ? KV_F16_MAX : 3.402823466e38f)) {
+        uint32_t top = kv_top<T>(raw);
+        if (live && top > __float_as_uint(DT == MILO_INT4 ? KV_F16_MAX : 3.402823466e38f)) {
             bad = true;
             top = 0u;
 #pragma unroll
@@ -307,9 +322,11 @@ template <typename T, int DT, int WPI> __global__ void __launch_bounds__(32 * KV
                 if (DT == MILO_INT4 && fabsf(r[i]) > KV_F16_MAX) r[i] = copysignf(KV_F16_MAX, r[i]);
                 top = max(top, __float_as_uint(r[i]) & 0x7fffffffu);
             }
+            if (kind == 0) bounds.add(r);
+        } else if (kind == 0 && live) {
+            bounds.add(raw, r);
         }
-        if (kind == 0) bounds.add(r);
-        kv_quant_store<DT>(r, __uint_as_float(top), j, mask, codes + (int64_t)t * ROW, par + (int64_t)t * PAR);
+        kv_quant_store<DT>(r, __uint_as_float(top), j, live, codes + (int64_t)t * ROW, par + (int64_t)t * PAR);
     }
     if (bad) raise_status(ST_NONFINITE);
     if (kind == 1) return;
@@ -361,30 +378,42 @@ template <typename T, int DT, int WPI> __global__ void __launch_bounds__(32 * KV
     if (wi == 0 && lane == 0) ((float *)a.c.section(l, 6))[blk] = sc;
 }
 
-// the value of a lane's 16 channels (16 j ..) of one row
-template <int DT>
-__device__ __forceinline__ void kv_dequant16(const unsigned char *codes, const unsigned char *par, int j,
-                                             float (&x)[16]) {
-    if constexpr (DT == MILO_INT4) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(codes) + j);
-        const __half2 p = __ldg(reinterpret_cast<const __half2 *>(par) + j / 2);   // (scale, zero)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint32_t c = ((i < 8 ? w.x : w.y) >> (4 * (i % 8))) & 15u;
-            x[i] = __half2float(__hfma(__ushort2half_rn((unsigned short)c), __low2half(p), __high2half(p)));
+// What a thread reads of one row: N channels' codes and their parameters
+template <int DT, int N> struct KvCodes {
+    uint32_t w[DT == MILO_INT4 ? (N + 7) / 8 : N / 4];
+    uint32_t p;                              // the scale's bits, or (scale, zero) of the channels' group
+
+    __device__ __forceinline__ void load(const unsigned char *codes, const unsigned char *par, int ch) {
+        if constexpr (DT == MILO_INT4) {
+            if constexpr (N == 8) w[0] = __ldg(reinterpret_cast<const uint32_t *>(codes) + ch / 8);
+            else w[0] = __ldg(reinterpret_cast<const uint16_t *>(codes) + ch / 4);
+            p = __ldg(reinterpret_cast<const uint32_t *>(par) + ch / KV_GROUP);
+        } else {
+            if constexpr (N == 8) {
+                const uint2 u = __ldg(reinterpret_cast<const uint2 *>(codes) + ch / 8);
+                w[0] = u.x;
+                w[1] = u.y;
+            } else {
+                w[0] = __ldg(reinterpret_cast<const uint32_t *>(codes) + ch / 4);
+            }
+            p = __ldg(reinterpret_cast<const uint32_t *>(par));
         }
-    } else {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(codes) + j);
-        const float s = __ldg(reinterpret_cast<const float *>(par));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        if constexpr (DT == MILO_INT8) {
+    }
+    __device__ __forceinline__ void get(float (&x)[N]) const {
+        if constexpr (DT == MILO_INT4) {
+            const __half2 sz = *reinterpret_cast<const __half2 *>(&p);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = __fmul_rn((float)(int8_t)(u[i / 4] >> (8 * (i % 4))), s);
+            for (int i = 0; i < N; ++i)
+                x[i] = __half2float(__hfma(__ushort2half_rn((unsigned short)((w[i / 8] >> (4 * (i % 8))) & 15u)),
+                                           __low2half(sz), __high2half(sz)));
+        } else if constexpr (DT == MILO_INT8) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = __fmul_rn((float)(int8_t)(w[i / 4] >> (8 * (i % 4))), __uint_as_float(p));
         } else {   // an e4m3's fields as an fp16's: the value times 2^-8, exactly
-            const float s8 = s * 256.f;
+            const float s8 = __uint_as_float(p) * 256.f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t v = __byte_perm(u[i / 2], 0u, i % 2 ? 0x3424 : 0x1404);
+            for (int i = 0; i < N / 2; ++i) {
+                const uint32_t v = __byte_perm(w[i / 2], 0u, i % 2 ? 0x3424 : 0x1404);
                 const uint32_t h = (v & 0x80008000u) | ((v >> 1) & 0x3f803f80u);
                 const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
                 x[2 * i] = __fmul_rn(f.x, s8);
@@ -392,7 +421,7 @@ __device__ __forceinline__ void kv_dequant16(const unsigned char *codes, const u
             }
         }
     }
-}
+};
 
 struct KvReadArgs {
     KvView c;
@@ -403,27 +432,44 @@ struct KvReadArgs {
 
 constexpr int KV_READ_ROWS = 64;
 
-// grid (L S H tiles, 2 kinds), 256 threads: eight threads a row, two rows each
+// grid (L S H tiles, 2 kinds), 256 threads.  A thread writes 16 bytes of a row, so
+// that the rows' threads write it in one piece, and takes several rows, whose
+// reads are issued together.
 template <typename T, int DT> __global__ void __launch_bounds__(256) k_kv_read(KvReadArgs a) {
+    constexpr int N = 16 / (int)sizeof(T), PER = D / N;       // channels of a thread, threads of a row
+    constexpr int STEP = 256 / PER, TAKE = KV_READ_ROWS / STEP;
+    constexpr int ROW = DT == MILO_INT4 ? D / 2 : D, PAR = DT == MILO_INT4 ? 4 * KV_NG : 4;
     const int kind = blockIdx.y;
     T *out = (T *)(kind ? a.v : a.k);
     if (!out) return;
-    constexpr int ROW = DT == MILO_INT4 ? D / 2 : D, PAR = DT == MILO_INT4 ? 4 * KV_NG : 4;
     const int tile = blockIdx.x % a.tiles, lsh = blockIdx.x / a.tiles;
     const int SH = a.c.S * a.c.H, l = lsh / SH, sh = lsh % SH, s = sh / a.c.H;
-    const int tid = threadIdx.x, j = tid & 7;
+    const int tid = threadIdx.x, ch = N * (tid % PER);
     int start, n;
     kv_range(a.start, a.count, s, a.n, a.c.cap, tid == 0 && tile == 0 && l == 0 && sh % a.c.H == 0, start, n);
-    const unsigned char *codes = a.c.codes(l, sh, kind) + (int64_t)start * ROW;
-    const unsigned char *par = a.c.params(l, sh, kind) + (int64_t)start * PAR;
-    out += (int64_t)lsh * a.n * D + 16 * j;
+    const int i0 = tile * KV_READ_ROWS + tid / PER;
+    const unsigned char *codes = a.c.codes(l, sh, kind) + (int64_t)(start + i0) * ROW;
+    const unsigned char *par = a.c.params(l, sh, kind) + (int64_t)(start + i0) * PAR;
+    out += ((int64_t)lsh * a.n + i0) * D + ch;
+    KvCodes<DT, N> c[TAKE];
 #pragma unroll
-    for (int y = 0; y < KV_READ_ROWS / 32; ++y) {
-        const int i = tile * KV_READ_ROWS + 32 * y + (tid >> 3);
-        if (i < n) {
-            float x[16];
-            kv_dequant16<DT>(codes + (int64_t)i * ROW, par + (int64_t)i * PAR, j, x);
-            kv_store16<T>(out + (int64_t)i * D, x);
+    for (int y = 0; y < TAKE; ++y)
+        if (i0 + STEP * y < n) c[y].load(codes + STEP * y * ROW, par + STEP * y * PAR, ch);
+#pragma unroll
+    for (int y = 0; y < TAKE; ++y) {
+        if (i0 + STEP * y < n) {
+            float x[N];
+            c[y].get(x);
+            uint4 w;
+            if constexpr (sizeof(T) == 4) {
+                w = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+            } else {
+                __nv_bfloat162 b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+                w = *reinterpret_cast<const uint4 *>(b);
+            }
+            *reinterpret_cast<uint4 *>(out + (int64_t)STEP * y * D) = w;
         }
     }
 }
