@@ -149,14 +149,16 @@ struct KvAttnPlan {
 KvAttnPlan kv_attn_plan(const milo_kv_shape *s, int32_t n_q, int32_t Hq, int32_t n_sel) {
     KvAttnPlan p{};
     const int64_t G = Hq / s->H, rows = n_sel ? G : G * n_q;
-    p.nt = rows <= 8 ? 1 : 2;
+    // up to 8 rows: two CTAs an SM, bound by memory; up to 16, and selected blocks, whose lines have few rows: two tiles
+    // of 8 a warp; above, 128 rows share a pass (17 queries of 7 heads over e4m3: 102 us in tiles of 16 rows, WIDE_US wide)
+    p.nt = rows <= 8 ? 1 : rows <= 16 || n_sel ? 2 : 16;
     const int rpt = 8 * p.nt;
     p.row_tiles = (int)((rows + rpt - 1) / rpt);
     p.classes = (int)((int64_t)s->S * (n_sel ? n_q : 1) * p.row_tiles);   // at most the query rows
     // units at most: a CTA with none would have nothing to do
-    const int warps = p.nt == 1 ? KaShape<1>::WARPS : KaShape<2>::WARPS;
-    const int begin = p.nt == 1 ? KaShape<1>::BEGIN : KaShape<2>::BEGIN;
-    const int ctas = p.nt == 1 ? KaShape<1>::CTAS : KaShape<2>::CTAS;
+    const int warps = p.nt == 1 ? KaShape<1>::WARPS : p.nt == 2 ? KaShape<2>::WARPS : KaShape<16>::WARPS;
+    const int begin = p.nt == 1 ? KaShape<1>::BEGIN : p.nt == 2 ? KaShape<2>::BEGIN : KaShape<16>::BEGIN;
+    const int ctas = p.nt == 1 ? KaShape<1>::CTAS : p.nt == 2 ? KaShape<2>::CTAS : KaShape<16>::CTAS;
     const int64_t tiles = n_sel ? (int64_t)n_sel * (s->block_len / 16) : ((int64_t)s->cap + 15) / 16;
     const int64_t units = (int64_t)p.classes * s->L * s->H * (begin + (tiles + warps - 1) / warps);
     p.grid = (int)std::min<int64_t>(units, ctas * sm_count());
@@ -191,23 +193,35 @@ template <typename K> cudaError_t kv_smem(K kernel, size_t bytes, bool (&done)[6
     return e;
 }
 
+template <typename T, int NT, bool SEL> cudaError_t kv_attn_merge(const KvAttnArgs &a, int grid, cudaStream_t s) {
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || grid == 1) return e;
+    // many parts a line: a CTA per row, else one for 16 rows at most
+    const int64_t lines = (int64_t)a.classes * a.c.L * a.c.H;
+    const int rows = grid >= 16 * lines ? 8 * NT : (8 * NT + 15) / 16;
+    return kv_follow(k_kv_attn_merge<T, NT, SEL>, dim3(grid, rows), 32 * KA_MERGE_WARPS, a, s);
+}
+
 template <typename T, int DT, int NT, bool SEL> cudaError_t kv_attn_run(const KvAttnArgs &a, int grid, cudaStream_t s) {
     static bool done[64];
     const size_t smem = sizeof(KaSmem<T, DT, NT>);
     const cudaError_t e = kv_smem(k_kv_attn<T, DT, NT, SEL>, smem, done);
     if (e != cudaSuccess) return e;
     k_kv_attn<T, DT, NT, SEL><<<grid, 32 * KaShape<NT>::WARPS, smem, s>>>(a);
-    // many parts a line: a CTA per row, else one for the line
-    const int64_t lines = (int64_t)a.classes * a.c.L * a.c.H;
-    if (grid > 1) {
-        const cudaError_t m = kv_follow(k_kv_attn_merge<T, NT, SEL>, dim3(grid, grid >= 16 * lines ? 8 * NT : 1),
-                                        32 * KA_MERGE_WARPS, a, s);
-        if (m != cudaSuccess) return m;
-    }
-    return cudaGetLastError();
+    return kv_attn_merge<T, NT, SEL>(a, grid, s);
+}
+
+template <typename T, int DT> cudaError_t kv_attn_run_wide(const KvAttnArgs &a, int grid, cudaStream_t s) {
+    static bool done[64];
+    const size_t smem = sizeof(KwSmem<T>);
+    const cudaError_t e = kv_smem(k_kv_attn_wide<T, DT>, smem, done);
+    if (e != cudaSuccess) return e;
+    k_kv_attn_wide<T, DT><<<grid, KW_THREADS, smem, s>>>(a);
+    return kv_attn_merge<T, 16, false>(a, grid, s);
 }
 
 template <typename T, int DT> cudaError_t kv_attn_rows(const KvAttnArgs &a, int nt, int grid, cudaStream_t s) {
+    if (nt == 16) return kv_attn_run_wide<T, DT>(a, grid, s);
     if (a.sel) return nt == 1 ? kv_attn_run<T, DT, 1, true>(a, grid, s) : kv_attn_run<T, DT, 2, true>(a, grid, s);
     return nt == 1 ? kv_attn_run<T, DT, 1, false>(a, grid, s) : kv_attn_run<T, DT, 2, false>(a, grid, s);
 }

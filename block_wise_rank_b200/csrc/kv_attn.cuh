@@ -53,8 +53,9 @@ struct KvAttnArgs {
 };
 
 // CTA shape by the query tiles of a warp: 8 NT rows
+// (16: the wide kernel's 128 rows)
 template <int NT> struct KaShape {
-    static constexpr int WARPS = NT == 1 ? 8 : 4, CTAS = NT == 1 ? 2 : 3;   // warps of a CTA, CTAs of an SM
+    static constexpr int WARPS = NT == 2 ? 4 : 8, CTAS = NT == 1 ? 2 : NT == 2 ? 3 : 1;   // warps of a CTA, CTAs of an SM
     static constexpr int BEGIN = NT == 1 ? 1 : 2;   // units that beginning and ending a line costs, counted at its front
 };
 constexpr float KA_RAISE = 4.f;        // a score this far above the reference raises it
@@ -346,6 +347,102 @@ template <bool SEL, int NT> struct KaClass {
     }
 };
 
+// A CTA's run of units [u0, u1) of the flattened lines, and the line that it is at.
+struct KaScan {
+    int64_t sum[32], off;
+    int cls;
+};
+template <bool SEL, int NT> struct KaRun {
+    static constexpr int THREADS = 32 * KaShape<NT>::WARPS;
+    KaClass<SEL, NT> cl;
+    int64_t u0, u1, n_units, line0;    // n_units: of every CTA; line0: first unit of the line
+    int k, per, l, h;                  // class, units of its lines, the line's layer and head
+
+    // Finds the run (the whole CTA calls it); false if it is empty.
+    __device__ __forceinline__ bool begin(const KvAttnArgs &a, KaScan &sc) {
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, LH = a.c.L * a.c.H;
+        int64_t total;
+        if (SEL) {
+            cl.set(a, 0, false);
+            total = (int64_t)a.classes * LH * cl.units(a);
+        } else {
+            const int chunk = (a.classes + THREADS - 1) / THREADS;
+            const int k0 = (int)min((int64_t)a.classes, (int64_t)tid * chunk), k1 = min(a.classes - k0, chunk) + k0;
+            int64_t mine = 0;
+            for (int i = k0; i < k1; ++i) {
+                cl.set(a, i, blockIdx.x == 0);   // each class once
+                mine += (int64_t)cl.units(a) * LH;
+            }
+            int64_t inc = mine;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            if (lane == 31) sc.sum[warp] = inc;
+            __syncthreads();
+            int64_t before = 0;
+            total = 0;
+            for (int w = 0; w < THREADS / 32; ++w) {
+                if (w < warp) before += sc.sum[w];
+                total += sc.sum[w];
+            }
+            int64_t at = before + inc - mine;    // first unit of class k0
+            const int64_t n = (total + gridDim.x - 1) / gridDim.x, u = blockIdx.x * n;
+            if (u >= at && u < at + mine) {
+                int i = k0;
+                for (;; ++i) {
+                    cl.set(a, i, false);
+                    const int64_t w = (int64_t)cl.units(a) * LH;
+                    if (u < at + w) break;
+                    at += w;
+                }
+                sc.cls = i;
+                sc.off = at;
+            }
+            __syncthreads();
+        }
+        n_units = (total + gridDim.x - 1) / gridDim.x;
+        u0 = blockIdx.x * n_units;
+        u1 = min(total, u0 + n_units);
+        if (u0 >= u1) return false;
+        int64_t cls0;
+        if (SEL) {
+            const int64_t w = (int64_t)cl.units(a) * LH;
+            k = (int)(u0 / w);
+            cls0 = k * w;
+        } else {
+            k = sc.cls;
+            cls0 = sc.off;
+        }
+        cl.set(a, k, SEL && tid == 0);
+        per = cl.units(a);
+        const int lh = (int)((u0 - cls0) / per);
+        line0 = cls0 + (int64_t)lh * per;
+        l = lh / a.c.H;
+        h = lh % a.c.H;
+        return true;
+    }
+    // this segment's units [s0, s1) of the line
+    __device__ __forceinline__ int s0() const { return (int)(u0 - line0); }
+    __device__ __forceinline__ int s1() const { return (int)min((int64_t)per, u1 - line0); }
+    // a line begun here and ended by a later CTA, for the merge
+    __device__ __forceinline__ int4 split() const { return make_int4(k, l, h, (int)((line0 + per - 1) / n_units)); }
+    __device__ __forceinline__ void next(const KvAttnArgs &a, int s1) {
+        u0 = line0 + s1;
+        if (s1 < per) return;
+        line0 += per;
+        if (++h < a.c.H) return;
+        h = 0;
+        if (++l < a.c.L) return;
+        l = 0;
+        if (u0 < u1) {
+            ++k;
+            cl.next(a, SEL && threadIdx.x == 0);
+            per = cl.units(a);
+        }
+    }
+};
+
 template <typename T, int DT, int NT> struct KaSmem {
     static constexpr int RPT = 8 * NT;                       // query rows of a line
     static constexpr int KA_WARPS = KaShape<NT>::WARPS;
@@ -358,13 +455,17 @@ template <typename T, int DT, int NT> struct KaSmem {
     float sc[RPT];                                           // factor on a row's scores
     int seen[RPT];
     int t0[KA_WARPS][KaTile<DT>::STAGES];                    // first token of the tile in each stage
-    int64_t scan[KA_WARPS + 1];
-    int cls;
-    int64_t off;
+    KaScan scan;
 };
 
-// Channels 4 lane .. of one finished row: normalised output; lane 0 adds lse / (max, sum) from the
-// reference m and the sum l in powers of two
+// lse / (max, sum) of one finished row, from the reference m and the sum l in powers of two
+__device__ __forceinline__ void ka_finish_sums(const KvAttnArgs &a, int64_t row, float m, float l) {
+    const float ln2 = 0.693147180559945309f;
+    if (a.lse) a.lse[row] = l != 0.f ? (m + log2f(l)) * ln2 : -INFINITY;
+    if (a.ml) a.ml[row] = l != 0.f ? make_float2(m * ln2, l) : make_float2(-INFINITY, 0.f);
+}
+
+// Channels 4 lane .. of one finished row: normalised output; lane 0 adds the sums
 template <typename T>
 __device__ __forceinline__ void ka_finish(const KvAttnArgs &a, int64_t row, int lane, float4 o, float m, float l) {
     if constexpr (sizeof(T) == 4) {
@@ -374,11 +475,7 @@ __device__ __forceinline__ void ka_finish(const KvAttnArgs &a, int64_t row, int 
         reinterpret_cast<uint2 *>(a.out)[row * (D / 4) + lane] =
             make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
     }
-    if (lane == 0) {
-        const float ln2 = 0.693147180559945309f;
-        if (a.lse) a.lse[row] = l != 0.f ? (m + log2f(l)) * ln2 : -INFINITY;
-        if (a.ml) a.ml[row] = l != 0.f ? make_float2(m * ln2, l) : make_float2(-INFINITY, 0.f);
-    }
+    if (lane == 0) ka_finish_sums(a, row, m, l);
 }
 
 template <typename T, int DT, int NT, bool SEL>
@@ -391,76 +488,17 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
     extern __shared__ __align__(16) unsigned char ka_raw[];
     Sm &sm = *reinterpret_cast<Sm *>(ka_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
-    const int LH = a.c.L * a.c.H;
-
-    // this CTA's run of units [u0, u1) and the class that u0 falls into
-    int64_t total;
-    KaClass<SEL, NT> cl;
-    if (SEL) {
-        cl.set(a, 0, false);
-        total = (int64_t)a.classes * LH * cl.units(a);
-    } else {
-        const int per = (a.classes + KA_THREADS - 1) / KA_THREADS;
-        const int k0 = (int)min((int64_t)a.classes, (int64_t)tid * per), k1 = min(a.classes - k0, per) + k0;
-        int64_t mine = 0;
-        for (int k = k0; k < k1; ++k) {
-            cl.set(a, k, blockIdx.x == 0);   // each class once
-            mine += (int64_t)cl.units(a) * LH;
-        }
-        int64_t inc = mine;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += x;
-        }
-        if (lane == 31) sm.scan[warp] = inc;
-        __syncthreads();
-        int64_t before = 0;
-        total = 0;
-        for (int w = 0; w < KA_WARPS; ++w) {
-            if (w < warp) before += sm.scan[w];
-            total += sm.scan[w];
-        }
-        int64_t at = before + inc - mine;                    // first unit of class k0
-        const int64_t n = (total + gridDim.x - 1) / gridDim.x, u = blockIdx.x * n;
-        if (u >= at && u < at + mine) {
-            int k = k0;
-            for (;; ++k) {
-                cl.set(a, k, false);
-                const int64_t w = (int64_t)cl.units(a) * LH;
-                if (u < at + w) break;
-                at += w;
-            }
-            sm.cls = k;
-            sm.off = at;
-        }
-        __syncthreads();
-    }
-    const int64_t n_units = (total + gridDim.x - 1) / gridDim.x;
-    int64_t u0 = blockIdx.x * n_units;
-    const int64_t u1 = min(total, u0 + n_units);
+    KaRun<SEL, NT> run;
+    const bool any_work = run.begin(a, sm.scan);
     if (tid == 0) a.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
     kv_launch_next();
-    if (u0 >= u1) return;
-    int k;                                                   // class, its first unit
-    int64_t cls0;
-    if (SEL) {
-        const int64_t w = (int64_t)cl.units(a) * LH;
-        k = (int)(u0 / w);
-        cls0 = k * w;
-    } else {
-        k = sm.cls;
-        cls0 = sm.off;
-    }
-    cl.set(a, k, SEL && tid == 0);
-    int per = cl.units(a);
-    const int lh = (int)((u0 - cls0) / per);                 // line of the class, its first unit
-    int64_t line0 = cls0 + (int64_t)lh * per;
-    int l = lh / a.c.H, h = lh % a.c.H;
+    if (!any_work) return;
+    const KaClass<SEL, NT> &cl = run.cl;
     float *const my_o = reinterpret_cast<float *>(sm.ring[warp]);
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(sm.ring[warp]);
 
-    while (u0 < u1) {
-        const int s0 = (int)(u0 - line0), s1 = (int)min((int64_t)per, u1 - line0);   // this segment's units of the line
+    while (run.u0 < run.u1) {
+        const int s0 = run.s0(), s1 = run.s1(), l = run.l, h = run.h;
         const int64_t sh = (int64_t)cl.s * a.c.H + h;
         const KaLine<DT> ln{a.c.codes(l, sh, 0), a.c.codes(l, sh, 1), a.c.params(l, sh, 0), a.c.params(l, sh, 1)};
         const int32_t *sel = SEL ? a.sel + ((((int64_t)l * a.c.S + cl.s) * a.n_q + cl.i) * a.c.H + h) * a.n_sel : nullptr;
@@ -708,7 +746,7 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
             }
         if (lane == 0) sm.e[warp] = PAR ? e_max : 1.f;
         __syncthreads();
-        const bool whole = s0 == 0 && s1 == per;
+        const bool whole = s0 == 0 && s1 == run.per;
         const int64_t part = 2 * (int64_t)blockIdx.x + (s0 == 0 ? 1 : 0);
         if (tid < RPT) {                                     // each warp's share of a row
             float e_top = 0.f, m = -INFINITY, den = 0.f;
@@ -750,24 +788,9 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
                 if (lane == 0) a.part_ml[part * RPT + r] = make_float2(sm.sc[r], sm.l[0][r]);
             }
         }
-        if (!whole && s0 == 0 && tid == 0)                   // begun here, ended by a later CTA
-            a.split[blockIdx.x] = make_int4(k, l, h, (int)((line0 + per - 1) / n_units));
+        if (!whole && s0 == 0 && tid == 0) a.split[blockIdx.x] = run.split();
         __syncthreads();                                     // queries and outputs used before the next segment
-        u0 = line0 + s1;
-        if (s1 == per) {                                     // next line
-            line0 += per;
-            if (++h == a.c.H) {
-                h = 0;
-                if (++l == a.c.L) {
-                    l = 0;
-                    if (u0 < u1) {
-                        ++k;
-                        cl.next(a, SEL && tid == 0);
-                        per = cl.units(a);
-                    }
-                }
-            }
-        }
+        run.next(a, s1);
     }
 }
 

@@ -30,7 +30,7 @@
 #include "decode_offload.cuh"
 #include "bm25.cuh"
 #include "rope.cuh"
-#include "kv_attn.cuh"
+#include "kv_attn_wide.cuh"
 
 using namespace milo;
 

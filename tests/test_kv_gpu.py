@@ -461,6 +461,42 @@ def test_attn_several_queries(dtype, dt, n_q, G):
 
 @pytest.mark.parametrize("dtype", KINDS)
 @pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("n_q,G,H", [(40, 7, 1), (1, 20, 2), (128, 1, 2), (129, 1, 1), (5, 4, 3)])
+def test_attn_many_query_rows(dtype, dt, n_q, G, H):
+    """More than 16 rows a line, below, at and above one tile of 128, over many tiles of tokens."""
+    length = [3000, 0, 1500, n_q, 127, 128, 129]
+    c = filled(1, len(length), H, 3000, 32, dtype, length)
+    check_attn(c, rnd(43, 1, len(length), n_q, G * H, 128, dtype=dt), length)
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_attn_many_query_rows_large_and_small_values(dtype, dt):
+    """The references and the value scales rise along the tiles: the output is rescaled."""
+    L, S, H, n, n_q = 1, 2, 1, 900, 24
+    c = make(L, S, H, n, 16, dtype)
+    k, v = rnd(44, L, S, H, n, 128), rnd(45, L, S, H, n, 128)
+    k *= torch.linspace(0.5, 6, n).cuda()[:, None]
+    if dtype != "int4":
+        v *= torch.exp2(torch.linspace(-30, 30, n).round()).cuda()[:, None]
+    k[0, 0, 0, 5], v[0, 0, 0, 7], k[0, 1] = 0.0, 0.0, 0.0
+    append(c, k, v, [0] * S)
+    q = rnd(46, L, S, n_q, 2, 128, dtype=dt)
+    q[0, 0, 3] *= 30.0
+    q[0, 0, 4] *= 1e-20
+    q[0, 0, 5] = 0.0
+    check_attn(c, q, [n, 333])
+    q[0, 0, 6, 1, 9], q[0, 0, 7, 0, 0] = math.nan, math.inf
+    out, lse = milo.milo_kv_attn(c, q, i32([n, 333]), return_lse=True)
+    ref, rl = milo.milo_kv_attn(c, torch.where(torch.isfinite(q), q, 0.0), i32([n, 333]), return_lse=True)
+    bad = ~torch.isfinite(q).all(-1)
+    assert torch.equal(out[~bad], ref[~bad]) and torch.equal(lse[~bad], rl[~bad])
+    assert int(bad.sum()) == 2 and not torch.isfinite(out[bad]).any() and not torch.isfinite(lse[bad]).any()
+    ok()
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+@pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("bl,n_q,G", [(16, 1, 7), (48, 2, 3), (64, 1, 8), (128, 1, 12)])
 def test_attn_selected_blocks(dtype, dt, bl, n_q, G):
     L, S, H, cap = 2, 4, 2, 700
