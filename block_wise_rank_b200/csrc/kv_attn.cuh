@@ -347,6 +347,11 @@ template <bool SEL, int NT> struct KaClass {
     }
 };
 
+// a / b, both not negative: a 64-bit division takes several times as long as a 32-bit one, and the units nearly always fit
+__device__ __forceinline__ int64_t ka_div(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // A CTA's run of units [u0, u1) of the flattened lines, and the line that it is at.
 struct KaScan {
     int64_t sum[32], off;
@@ -387,7 +392,7 @@ template <bool SEL, int NT> struct KaRun {
                 total += sc.sum[w];
             }
             int64_t at = before + inc - mine;    // first unit of class k0
-            const int64_t n = (total + gridDim.x - 1) / gridDim.x, u = blockIdx.x * n;
+            const int64_t n = ka_div(total + gridDim.x - 1, gridDim.x), u = blockIdx.x * n;
             if (u >= at && u < at + mine) {
                 int i = k0;
                 for (;; ++i) {
@@ -401,14 +406,14 @@ template <bool SEL, int NT> struct KaRun {
             }
             __syncthreads();
         }
-        n_units = (total + gridDim.x - 1) / gridDim.x;
+        n_units = ka_div(total + gridDim.x - 1, gridDim.x);
         u0 = blockIdx.x * n_units;
         u1 = min(total, u0 + n_units);
         if (u0 >= u1) return false;
         int64_t cls0;
         if (SEL) {
             const int64_t w = (int64_t)cl.units(a) * LH;
-            k = (int)(u0 / w);
+            k = (int)ka_div(u0, w);
             cls0 = k * w;
         } else {
             k = sc.cls;
@@ -416,7 +421,7 @@ template <bool SEL, int NT> struct KaRun {
         }
         cl.set(a, k, SEL && tid == 0);
         per = cl.units(a);
-        const int lh = (int)((u0 - cls0) / per);
+        const int lh = (int)ka_div(u0 - cls0, per);
         line0 = cls0 + (int64_t)lh * per;
         l = lh / a.c.H;
         h = lh % a.c.H;
@@ -426,7 +431,7 @@ template <bool SEL, int NT> struct KaRun {
     __device__ __forceinline__ int s0() const { return (int)(u0 - line0); }
     __device__ __forceinline__ int s1() const { return (int)min((int64_t)per, u1 - line0); }
     // a line begun here and ended by a later CTA, for the merge
-    __device__ __forceinline__ int4 split() const { return make_int4(k, l, h, (int)((line0 + per - 1) / n_units)); }
+    __device__ __forceinline__ int4 split() const { return make_int4(k, l, h, (int)ka_div(line0 + per - 1, n_units)); }
     __device__ __forceinline__ void next(const KvAttnArgs &a, int s1) {
         u0 = line0 + s1;
         if (s1 < per) return;
@@ -824,8 +829,9 @@ __global__ void __launch_bounds__(32 * KA_MERGE_WARPS) k_kv_attn_merge(const __g
             x[y] = make_float2(-INFINITY, 0.f);
             o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (i < n) {
-                x[y] = a.part_ml[at(i)];
+                x[y] = a.part_ml[at(i)];                     // a sum of 0: an empty part, whose output may not be written
                 o[y] = *reinterpret_cast<const float4 *>(a.part_o + at(i) * D + 4 * lane);
+                if (x[y].y == 0.f) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
         float top = m;

@@ -9,7 +9,7 @@
 //     and values, MN-major, alike), two buffers deep;
 //   - S = Q K^T, M = N = 128, fp32 in tensor memory, Q in one (bf16) or two
 //     (fp32) fp16 parts from shared memory;
-//   - each thread takes half of one query row's scores: scales, mask,
+//   - each thread takes a quarter of one query row's scores: scales, mask,
 //     running reference and sum as in k_kv_attn, the weights packed to fp16
 //     parts back into tensor memory;
 //   - O += P V with P from tensor memory, while the next tile's S is formed.
@@ -22,7 +22,10 @@
 
 namespace milo {
 
-constexpr int KW_ROWS = 128, KW_TOK = 128, KW_THREADS = 256;
+constexpr int KW_ROWS = 128, KW_TOK = 128, KW_THREADS = 512;
+static_assert(KW_TOK == D, "a thread's columns of the scores are also its columns of the output");
+constexpr int KW_SPLIT = KW_THREADS / KW_ROWS, KW_COLS = KW_TOK / KW_SPLIT;   // threads of a query row, tokens of each
+constexpr int KW_WARPS = KW_THREADS / 32, KW_TAKE = KW_TOK * 8 / KW_THREADS;  // 16-channel pieces of a tile that a thread widens
 constexpr uint32_t KW_TMEM = 512, KW_S = 0, KW_O = 128, KW_P = 256;   // columns: scores, output, weights (2 parts of 64)
 constexpr int KW_TILE = KW_TOK * D * 2;                               // bytes of a widened tile
 
@@ -31,7 +34,7 @@ template <typename T> struct KwSmem {
     unsigned char q[PARTS][KW_TILE], k[2][KW_TILE], v[2][KW_TILE];
     float ks[2][KW_TOK], vs[2][KW_TOK];       // scales of a tile's rows
     float top[2][4];                          // greatest value scale of 32 rows each
-    float x[2][KW_ROWS];                      // exchange between a row's two threads
+    float x[KW_SPLIT][KW_ROWS];               // exchange between a row's threads
     float sc[KW_ROWS];
     int seen[KW_ROWS];
     KaScan scan;
@@ -39,27 +42,45 @@ template <typename T> struct KwSmem {
     uint32_t tmem;
 };
 
-// A thread's share of a tile: 4 times 16 channels of a row (row kw_row(j), channels 16 kw_c16(j) ..), and one row's scales
-__device__ __forceinline__ int kw_row(int j) { return 8 * ((threadIdx.x / 32 + 8 * j) / 2) + threadIdx.x % 8; }
-__device__ __forceinline__ int kw_c16(int j) { return 4 * ((threadIdx.x / 32 + 8 * j) % 2) + (threadIdx.x % 32) / 8; }
+// A thread's share of a tile: KW_TAKE times 16 channels of a row (row kw_row(j), channels 16 kw_c16(j) ..)
+__device__ __forceinline__ int kw_row(int j) { return 8 * ((threadIdx.x / 32 + KW_WARPS * j) / 2) + threadIdx.x % 8; }
+__device__ __forceinline__ int kw_c16(int j) { return 4 * ((threadIdx.x / 32 + KW_WARPS * j) % 2) + (threadIdx.x % 32) / 8; }
+
+// Loads that stay where they are written: their results are used a tile later, and a load that may be moved is moved
+// behind the wait that it is meant to pass
+__device__ __forceinline__ uint4 kw_ldg16(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint2 kw_ldg8(const void *p) {
+    uint2 v;
+    asm volatile("ld.global.nc.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint32_t kw_ldg4(const void *p) {
+    uint32_t v;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
 
 template <int DT> struct KwRaw {
-    uint4 w[4];                               // 4 bits: x and y
-    uint32_t p[DT == MILO_INT4 ? 4 : 1];      // 4 bits: (scale, zero) of the channels' group
+    uint4 w[KW_TAKE];                         // 4 bits: x and y
+    uint32_t p[DT == MILO_INT4 ? KW_TAKE : 1];      // 4 bits: (scale, zero) of the channels' group
     __device__ __forceinline__ void load(const unsigned char *codes, const unsigned char *par, int t0, int end) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < KW_TAKE; ++j) {
             const int64_t t = t0 + kw_row(j);
             w[j] = make_uint4(0u, 0u, 0u, 0u);
             if (DT == MILO_INT4) p[j] = 0u;
             if (t < end) {
                 if constexpr (DT == MILO_INT4) {
-                    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(codes + t * 64) + kw_c16(j));
+                    const uint2 u = kw_ldg8(codes + t * 64 + 8 * kw_c16(j));
                     w[j].x = u.x;
                     w[j].y = u.y;
-                    p[j] = __ldg(reinterpret_cast<const uint32_t *>(par + t * 16) + kw_c16(j) / 2);
+                    p[j] = kw_ldg4(par + t * 16 + 4 * (kw_c16(j) / 2));
                 } else {
-                    w[j] = __ldg(reinterpret_cast<const uint4 *>(codes + t * 128) + kw_c16(j));
+                    w[j] = kw_ldg16(codes + t * 128 + 16 * kw_c16(j));
                 }
             }
         }
@@ -68,7 +89,7 @@ template <int DT> struct KwRaw {
     // 0 4 1 5 2 6 3 7 of each 8 channels (kw_order).
     __device__ __forceinline__ void store(unsigned char *tile) const {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < KW_TAKE; ++j) {
             uint32_t o[8];
             if constexpr (DT == MILO_INT4) {
                 const __half2 s = ka_h(__byte_perm(p[j], 0u, 0x1010)), z = ka_h(__byte_perm(p[j], 0u, 0x3232));
@@ -103,8 +124,8 @@ template <int DT> struct KwRaw {
 // channel (of 8) at place p of a widened row
 template <int DT> __device__ __forceinline__ constexpr int kw_order(int p) { return DT == MILO_INT4 ? p / 2 + 4 * (p % 2) : p; }
 
-__device__ __forceinline__ void kw_pair_sync(int warp) {   // the two warps that share 32 query rows
-    asm volatile("bar.sync %0, 64;" ::"r"(1 + warp % 4) : "memory");
+__device__ __forceinline__ void kw_rows_sync(int warp) {   // the warps that share 32 query rows
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + warp % 4), "n"(32 * KW_SPLIT) : "memory");
 }
 
 template <typename T, int DT> __global__ void __launch_bounds__(KW_THREADS, 1) k_kv_attn_wide(const __grid_constant__ KvAttnArgs a) {
@@ -134,7 +155,7 @@ template <typename T, int DT> __global__ void __launch_bounds__(KW_THREADS, 1) k
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    const int row = 32 * (warp % 4) + lane, half = warp / 4;       // this thread's query row and half of a tile's tokens
+    const int row = 32 * (warp % 4) + lane, col = KW_COLS * (warp / 4);   // this thread's query row and first token of a tile
     const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;      // its warp's tensor-memory lanes
     const uint32_t sq = tc::smem_u32(sm.q), sk = tc::smem_u32(sm.k), sv = tc::smem_u32(sm.v);
     uint32_t n_s = 0, n_o = 0;                                     // phases of the two barriers
@@ -165,6 +186,14 @@ template <typename T, int DT> __global__ void __launch_bounds__(KW_THREADS, 1) k
         const unsigned char *kp = a.c.params(l, sh, 0), *vp = a.c.params(l, sh, 1);
         const int first = max(s0 - BEGIN, 0), end = cl.end;        // tiles [first, first + n)
         const int n = max(min((end + KW_TOK - 1) / KW_TOK, s1 - BEGIN) - first, 0);
+        const bool whole = s0 == 0 && s1 == run.per;
+        const int64_t part = 2 * (int64_t)blockIdx.x + (s0 == 0 ? 1 : 0);
+        if (n == 0 && !whole) {                                    // the units that stand for a line's begin alone
+            if (tid < KW_ROWS) a.part_ml[part * KW_ROWS + tid] = make_float2(-INFINITY, 0.f);
+            if (s0 == 0 && tid == 0) a.split[blockIdx.x] = run.split();
+            run.next(a, s1);
+            continue;
+        }
         KwRaw<DT> rk, rv;
         float rks = 0.f, rvs = 0.f;
         auto load_k = [&](int i) { rk.load(kc, kp, (first + i) * KW_TOK, end); };
@@ -172,8 +201,11 @@ template <typename T, int DT> __global__ void __launch_bounds__(KW_THREADS, 1) k
             rv.load(vc, vp, (first + i) * KW_TOK, end);
             if (PAR && tid < KW_TOK) {
                 const int t = (first + i) * KW_TOK + tid;
-                rks = t < end ? __ldg(reinterpret_cast<const float *>(kp) + t) : 0.f;
-                rvs = t < end ? __ldg(reinterpret_cast<const float *>(vp) + t) : 0.f;
+                rks = rvs = 0.f;
+                if (t < end) {
+                    rks = __uint_as_float(kw_ldg4(kp + 4 * (int64_t)t));
+                    rvs = __uint_as_float(kw_ldg4(vp + 4 * (int64_t)t));
+                }
             }
         };
         auto store_scales = [&](int buf) {
@@ -191,18 +223,26 @@ template <typename T, int DT> __global__ void __launch_bounds__(KW_THREADS, 1) k
         // the queries, eight rows a warp: a lane holds 8-channel chunks x, x + 4, x + 8, x + 12 of its row
         const int x = lane / 8;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const int r = 8 * (warp + 8 * g) + lane % 8;
+        for (int g = 0; g < 16 / KW_WARPS; ++g) {
+            const int r = 8 * (warp + KW_WARPS * g) + lane % 8;
             const bool live = r < cl.rows;
             float q[4][8], mx = 0.f;
             const T *src = (const T *)a.q + (live ? cl.row(a, l, h, r) : 0) * D;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                uint4 w[sizeof(T) / 2];                            // 8 channels
+#pragma unroll
+                for (int e = 0; e < (int)sizeof(T) / 2; ++e) {
+                    w[e] = make_uint4(0u, 0u, 0u, 0u);
+                    if (live) w[e] = __ldg(reinterpret_cast<const uint4 *>(src + 8 * (x + 4 * i)) + e);
+                }
+                const T *t = reinterpret_cast<const T *>(w);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    q[i][e] = live ? to_f32(src[8 * (x + 4 * i) + kw_order<DT>(e)]) : 0.f;
+                    q[i][e] = to_f32(t[kw_order<DT>(e)]);
                     mx = fmaxf(mx, fabsf(q[i][e]));
                 }
+            }
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             const int e2 = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 127);
@@ -249,7 +289,7 @@ template <typename T, int DT> __global__ void __launch_bounds__(KW_THREADS, 1) k
         float ref = -INFINITY, sum = 0.f, e_max = 0.f, e_inv = 0.f;
 
         for (int i = 0; i < n; ++i) {
-            const int buf = i & 1, t0 = (first + i) * KW_TOK + 64 * half;
+            const int buf = i & 1, t0 = (first + i) * KW_TOK + col;
             if (i + 1 < n) {
                 rk.store(sm.k[buf ^ 1]);                           // S of the tile before it is formed
                 if (i + 2 < n) load_k(i + 2);
@@ -257,39 +297,39 @@ template <typename T, int DT> __global__ void __launch_bounds__(KW_THREADS, 1) k
             ok = tc::mbar_wait(&sm.bar_s, n_s & 1u) && ok;
             ++n_s;
             tc::tc_fence_after();
-            float z[64];
+            float z[KW_COLS];
             float fac = 1.f;
             bool rescale = false;
             if (!idle) {
                 float top = -INFINITY;
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    uint32_t r[32];
-                    tc::tmem_ld32(tmem + KW_S + lanes + 64 * half + 32 * b, r);
+                {
+                    uint32_t r[KW_COLS];
+                    tc::tmem_ld32(tmem + KW_S + lanes + col, r);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
+                    for (int c = 0; c < KW_COLS; c += 4) {
                         float4 f = make_float4(sc, sc, sc, sc);
                         if (PAR) {
-                            const float4 k4 = *reinterpret_cast<const float4 *>(&sm.ks[buf][64 * half + 32 * b + c]);
+                            const float4 k4 = *reinterpret_cast<const float4 *>(&sm.ks[buf][col + c]);
                             f = make_float4(k4.x * sc, k4.y * sc, k4.z * sc, k4.w * sc);
                         }
-                        z[32 * b + c] = __uint_as_float(r[c]) * f.x;
-                        z[32 * b + c + 1] = __uint_as_float(r[c + 1]) * f.y;
-                        z[32 * b + c + 2] = __uint_as_float(r[c + 2]) * f.z;
-                        z[32 * b + c + 3] = __uint_as_float(r[c + 3]) * f.w;
+                        z[c] = __uint_as_float(r[c]) * f.x;
+                        z[c + 1] = __uint_as_float(r[c + 1]) * f.y;
+                        z[c + 2] = __uint_as_float(r[c + 2]) * f.z;
+                        z[c + 3] = __uint_as_float(r[c + 3]) * f.w;
                     }
                 }
-                if (t0 + 64 > seen) {
+                if (t0 + KW_COLS > seen) {
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
+                    for (int c = 0; c < KW_COLS; ++c)
                         if (t0 + c >= seen) z[c] = -INFINITY;
                 }
 #pragma unroll
-                for (int c = 0; c < 64; ++c) top = fmaxf(top, z[c]);
-                sm.x[half][row] = top;
-                kw_pair_sync(warp);
-                top = fmaxf(top, sm.x[half ^ 1][row]);
+                for (int c = 0; c < KW_COLS; ++c) top = fmaxf(top, z[c]);
+                sm.x[warp / 4][row] = top;
+                kw_rows_sync(warp);
+#pragma unroll
+                for (int y = 0; y < KW_SPLIT; ++y) top = fmaxf(top, sm.x[y][row]);
                 if (top > ref + KA_RAISE) {
                     fac = ref == -INFINITY ? 0.f : ka_exp2(ref - top);
                     ref = top;
@@ -317,30 +357,27 @@ template <typename T, int DT> __global__ void __launch_bounds__(KW_THREADS, 1) k
             }
             if (!idle) {
                 if (i > 0 && __any_sync(0xffffffffu, rescale)) {
-#pragma unroll 1
-                    for (int b = 0; b < 2; ++b) {
-                        const uint32_t at = tmem + KW_O + lanes + 64 * half + 32 * b;
-                        uint32_t r[32];
-                        tc::tmem_ld32(at, r);
-                        tc::tmem_wait_ld();
+                    const uint32_t at = tmem + KW_O + lanes + col;   // as many columns of the output
+                    uint32_t r[KW_COLS];
+                    tc::tmem_ld32(at, r);
+                    tc::tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < 32; c += 8) {
-                            uint32_t w[8];
+                    for (int c = 0; c < KW_COLS; c += 8) {
+                        uint32_t w[8];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__uint_as_float(r[c + e]) * fac);
-                            tc::tmem_st8(at + c, w);
-                        }
+                        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__uint_as_float(r[c + e]) * fac);
+                        tc::tmem_st8(at + c, w);
                     }
                 }
                 const float off = KA_SHIFT - (ref == -INFINITY ? 0.f : ref);
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {                      // 16 tokens: 8 columns of each part
+                for (int b = 0; b < KW_COLS / 16; ++b) {           // 16 tokens: 8 columns of each part
                     uint32_t hi[8], lo[8];
 #pragma unroll
                     for (int c = 0; c < 16; c += 4) {
                         float p[4];
                         float4 w4 = make_float4(1.f, 1.f, 1.f, 1.f);
-                        if (PAR) w4 = *reinterpret_cast<const float4 *>(&sm.vs[buf][64 * half + 16 * b + c]);
+                        if (PAR) w4 = *reinterpret_cast<const float4 *>(&sm.vs[buf][col + 16 * b + c]);
                         const float w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -356,8 +393,8 @@ template <typename T, int DT> __global__ void __launch_bounds__(KW_THREADS, 1) k
                                 lo[c / 2 + e] = ka_u(__floats2half2_rn(p[2 * e] - __low2float(hh), p[2 * e + 1] - __high2float(hh)));
                         }
                     }
-                    tc::tmem_st8(tmem + KW_P + lanes + 32 * half + 8 * b, hi);
-                    if (PARTS == 2) tc::tmem_st8(tmem + KW_P + 64 + lanes + 32 * half + 8 * b, lo);
+                    tc::tmem_st8(tmem + KW_P + lanes + col / 2 + 8 * b, hi);
+                    if (PARTS == 2) tc::tmem_st8(tmem + KW_P + 64 + lanes + col / 2 + 8 * b, lo);
                 }
                 tc::tmem_wait_st();
             }
@@ -382,53 +419,44 @@ template <typename T, int DT> __global__ void __launch_bounds__(KW_THREADS, 1) k
             ++n_o;
             tc::tc_fence_after();
         }
-        // the row's two sums, then its output
-        sm.x[half][row] = sum;
+        // the row's sums, then its output
+        sm.x[warp / 4][row] = sum;
         ok = __syncthreads_and(ok);
         if (!ok) break;
-        const float den = sm.x[0][row] + sm.x[1][row];
-        const bool whole = s0 == 0 && s1 == run.per;
-        const int64_t part = 2 * (int64_t)blockIdx.x + (s0 == 0 ? 1 : 0);
+        float den = 0.f;
+#pragma unroll
+        for (int y = 0; y < KW_SPLIT; ++y) den += sm.x[y][row];
         const float inv = den != 0.f ? 1.f / den : 0.f, scale_o = (PAR ? e_max : 1.f) * UP;
-        const bool live = row < cl.rows;
-        const int64_t out_row = live ? cl.row(a, l, h, row) : 0;
+        // through shared memory (the tiles' place), so that a warp writes whole rows
+        float(*const out)[D + 4] = reinterpret_cast<float(*)[D + 4]>(sm.k);
+        static_assert(sizeof(float) * KW_ROWS * (D + 4) <= sizeof(sm.k) + sizeof(sm.v), "the output fits in the tiles' place");
         if (!idle) {
+            uint32_t r[KW_COLS];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                uint32_t r[32];
-#pragma unroll
-                for (int c = 0; c < 32; ++c) r[c] = 0u;
-                if (n > 0) {
-                    tc::tmem_ld32(tmem + KW_O + lanes + 64 * half + 32 * b, r);
-                    tc::tmem_wait_ld();
-                }
-                if (live) {
-                    float y[32];
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)   // den == 0: nothing seen, and the sums may be another row's leftovers
-                        y[c / 8 * 8 + kw_order<DT>(c % 8)] = den != 0.f ? __uint_as_float(r[c]) * inv * scale_o : 0.f;
-                    const int ch = 64 * half + 32 * b;
-                    if (!whole || sizeof(T) == 4) {
-                        float *to = whole ? (float *)a.out + out_row * D + ch : a.part_o + (part * KW_ROWS + row) * D + ch;
-#pragma unroll
-                        for (int c = 0; c < 32; c += 4)
-                            *reinterpret_cast<float4 *>(to + c) = make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]);
-                    } else {
-                        __nv_bfloat16 *to = (__nv_bfloat16 *)a.out + out_row * D + ch;
-#pragma unroll
-                        for (int c = 0; c < 32; c += 8) {
-                            __nv_bfloat162 w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) w[e] = __floats2bfloat162_rn(y[c + 2 * e], y[c + 2 * e + 1]);
-                            *reinterpret_cast<uint4 *>(to + c) = *reinterpret_cast<const uint4 *>(w);
-                        }
-                    }
-                }
+            for (int c = 0; c < KW_COLS; ++c) r[c] = 0u;
+            if (n > 0) {
+                tc::tmem_ld32(tmem + KW_O + lanes + col, r);
+                tc::tmem_wait_ld();
             }
-            if (live && half == 0) {
-                const float m = ref - KA_SHIFT;
-                if (whole) ka_finish_sums(a, out_row, m, den);
-                else a.part_ml[part * KW_ROWS + row] = make_float2(m, den);
+            float y[KW_COLS];
+#pragma unroll
+            for (int c = 0; c < KW_COLS; ++c)   // den == 0: nothing seen, and the sums may be another line's leftovers
+                y[c / 8 * 8 + kw_order<DT>(c % 8)] = den != 0.f ? __uint_as_float(r[c]) * inv * scale_o : 0.f;
+#pragma unroll
+            for (int c = 0; c < KW_COLS; c += 4)
+                *reinterpret_cast<float4 *>(&out[row][col + c]) = make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]);
+            if (warp < 4) {
+                sm.ks[0][row] = ref - KA_SHIFT;   // the scales are used up
+                sm.sc[row] = den;
+            }
+        }
+        __syncthreads();
+        for (int r = warp; r < cl.rows; r += KW_WARPS) {
+            const float4 y = *reinterpret_cast<const float4 *>(&out[r][4 * lane]);
+            if (whole) ka_finish<T>(a, cl.row(a, l, h, r), lane, y, sm.ks[0][r], sm.sc[r]);
+            else {
+                *reinterpret_cast<float4 *>(a.part_o + (part * KW_ROWS + r) * D + 4 * lane) = y;
+                if (lane == 0) a.part_ml[part * KW_ROWS + r] = make_float2(sm.ks[0][r], sm.sc[r]);
             }
         }
         if (!whole && s0 == 0 && tid == 0) a.split[blockIdx.x] = run.split();
