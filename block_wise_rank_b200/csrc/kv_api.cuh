@@ -150,7 +150,7 @@ KvAttnPlan kv_attn_plan(const milo_kv_shape *s, int32_t n_q, int32_t Hq, int32_t
     KvAttnPlan p{};
     const int64_t G = Hq / s->H, rows = n_sel ? G : G * n_q;
     // up to 8 rows: two CTAs an SM, bound by memory; up to 16, and selected blocks, whose lines have few rows: two tiles
-    // of 8 a warp; above, 128 rows share a pass (17 queries of 7 heads over e4m3: 102 us in tiles of 16 rows, WIDE_US wide)
+    // of 8 a warp; above, 128 rows share a pass (17 queries of 7 heads over e4m3: 102 us in tiles of 16 rows, 52 us wide)
     p.nt = rows <= 8 ? 1 : rows <= 16 || n_sel ? 2 : 16;
     const int rpt = 8 * p.nt;
     p.row_tiles = (int)((rows + rpt - 1) / rpt);

@@ -161,21 +161,28 @@ template <typename T, int DT> __global__ void __launch_bounds__(KW_THREADS, 1) k
     uint32_t n_s = 0, n_o = 0;                                     // phases of the two barriers
     bool ok = true;
 
-    auto issue_s = [&](int buf) {                                  // one thread
-        const uint32_t id = tc::idesc_f16(KW_ROWS, KW_TOK, 0, 0, 0);
+    // one thread issues; the descriptors of a product's steps differ by constants in their address field (16-byte units),
+    // so that a step costs an addition
+    const uint64_t d_q = tc::smem_desc(sq, 128, 2048, tc::LAYOUT_NONE), d_k = tc::smem_desc(sk, 128, 2048, tc::LAYOUT_NONE);
+    const uint64_t d_v = tc::smem_desc(sv, 2048, 128, tc::LAYOUT_NONE);
+    auto issue_s = [&](int buf) {
+        constexpr uint32_t id = tc::idesc_f16(KW_ROWS, KW_TOK, 0, 0, 0);
+        const uint64_t k = d_k + (uint64_t)(buf * (KW_TILE / 16));
+#pragma unroll
         for (int p = 0; p < PARTS; ++p)
+#pragma unroll
             for (int j = 0; j < D / 16; ++j)
-                tc::mma_ss(tmem + KW_S, tc::smem_desc(sq + p * KW_TILE + j * 256, 128, 2048, tc::LAYOUT_NONE),
-                           tc::smem_desc(sk + buf * KW_TILE + j * 256, 128, 2048, tc::LAYOUT_NONE), id, (p | j) != 0);
+                tc::mma_ss(tmem + KW_S, d_q + p * (KW_TILE / 16) + j * 16, k + j * 16, id, (p | j) != 0);
         tc::mma_commit(&sm.bar_s);
     };
     auto issue_o = [&](int buf, bool first) {
-        const uint32_t id = tc::idesc_f16(KW_ROWS, D, 0, 0, 1);
+        constexpr uint32_t id = tc::idesc_f16(KW_ROWS, D, 0, 0, 1);
+        const uint64_t v = d_v + (uint64_t)(buf * (KW_TILE / 16));
+#pragma unroll
         for (int p = 0; p < PARTS; ++p)
+#pragma unroll
             for (int j = 0; j < KW_TOK / 16; ++j)
-                tc::mma_ts(tmem + KW_O, tmem + KW_P + 64 * p + 8 * j,
-                           tc::smem_desc(sv + buf * KW_TILE + j * 4096, 2048, 128, tc::LAYOUT_NONE), id,
-                           !first || (p | j) != 0);
+                tc::mma_ts(tmem + KW_O, tmem + KW_P + 64 * p + 8 * j, v + j * 256, id, (p | j) != 0 || !first);
         tc::mma_commit(&sm.bar_o);
     };
 
