@@ -79,7 +79,8 @@ bool kv_ok(const milo_kv_shape *s) {
     return s && s->L > 0 && s->S > 0 && s->H > 0 && s->cap > 0 && s->cap <= (1 << 26) && s->block_len >= 16 &&
            s->block_len <= 1024 && s->block_len % 16 == 0 &&
            (s->dtype == MILO_INT8 || s->dtype == MILO_FP8 || s->dtype == MILO_INT4) &&
-           (int64_t)s->S * s->H <= INT32_MAX && (int64_t)s->L * s->S * s->H <= INT32_MAX;
+           (int64_t)s->S * s->H <= INT32_MAX && (int64_t)s->L * s->S * s->H <= INT32_MAX &&
+           (double)s->L * s->S * s->H * s->cap < 4e15;   // at most 600 bytes a row: sizes stay inside 64 bits
 }
 
 milo_status kv_check(const milo_kv_shape *s, const void *cache, size_t bytes) {

@@ -487,7 +487,7 @@ template <typename T, int DT, int NT, bool SEL>
 __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_kv_attn(const __grid_constant__ KvAttnArgs a) {
     using Sm = KaSmem<T, DT, NT>;
     using Tl = KaTile<DT>;
-    constexpr int RPT = Sm::RPT, PARTS = Sm::PARTS, KA_WARPS = Sm::KA_WARPS, KA_THREADS = 32 * KA_WARPS;
+    constexpr int RPT = Sm::RPT, PARTS = Sm::PARTS, KA_WARPS = Sm::KA_WARPS;
     constexpr int KA_BEGIN = KaShape<NT>::BEGIN;
     constexpr bool PAR = DT != MILO_INT4;                    // a scale per row
     extern __shared__ __align__(16) unsigned char ka_raw[];
@@ -558,8 +558,11 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
         for (int y = 0; y < RPT / KA_WARPS; ++y) {
             const int r = warp + y * KA_WARPS;
             const T *q = (const T *)a.q + cl.row(a, l, h, min(r, cl.rows - 1)) * D + 4 * lane;
+            T t[4];                                          // 16 or 8 bytes
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(t) = __ldg(reinterpret_cast<const uint4 *>(q));
+            else *reinterpret_cast<uint2 *>(t) = __ldg(reinterpret_cast<const uint2 *>(q));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) qx[y][e] = r < cl.rows ? to_f32(q[e]) : 0.f;
+            for (int e = 0; e < 4; ++e) qx[y][e] = r < cl.rows ? to_f32(t[e]) : 0.f;
         }
 #pragma unroll
         for (int y = 0; y < RPT / KA_WARPS; ++y) {

@@ -595,6 +595,11 @@ class KvCache:
         return KvCache(one, self.buf[l * n:(l + 1) * n])
 
 
+def _strides(t: torch.Tensor):
+    """t's strides; 0 where a dimension has one index (any stride is as good)."""
+    return tuple(0 if n == 1 else s for n, s in zip(t.shape, t.stride()))
+
+
 def milo_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, start: torch.Tensor, count=None,
                    stream=None) -> None:
     """Quantise k, v [L][S][H][n][d] (fp32 or bf16; any strides that k and v
@@ -604,8 +609,8 @@ def milo_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, start: torc
     if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 5 or \
             tuple(k.shape[:3]) != (c.L, c.S, c.H) or k.shape[4] != c.d:
         raise ValueError(f"k, v: [{c.L}][{c.S}][{c.H}][n][{c.d}] expected, got {tuple(k.shape)} and {tuple(v.shape)}")
-    st = k.stride()
-    if k.numel() and (st != v.stride() or st[4] != 1):
+    st = _strides(k)
+    if k.numel() and (st != _strides(v) or st[4] != 1):
         raise ValueError("k and v: equal strides and contiguous rows expected")
     s = _on(k, stream)
     _int32(start, (c.S,), "start")

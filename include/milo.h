@@ -31,6 +31,8 @@
  *     Jacobi sweep cap reached, non-finite input, a bad block id, a wait on
  *     the device that ran out) set bits
  *     of a per-device status word that milo_get_status reads and clears.
+ *   - A workspace belongs to one call at a time: calls, and graphs captured
+ *     from them, that may run at once take workspaces of their own.
  *   - No C++ exception crosses this interface.
  *   - d (head dimension) must be 128, except in milo_rope.
  */
@@ -408,7 +410,8 @@ milo_status milo_rope_freqs(const milo_rope_params *params, double *w, double *a
  *             x_dtype / y_dtype (MILO_F32 or MILO_BF16); row (t, h) starts at
  *             element t * token_stride + h * head_stride.  Strides of x are >= 0
  *             (0 reads a broadcast row); rows of y must not overlap.  y may be x
- *             (same type and strides); any other overlap is an error.
+ *             (same type and strides); otherwise the ranges from the first to the
+ *             last byte of x and y must be apart.
  *   positions:device, int32 [n_pos], any sign; n_pos >= 1 (n_tokens tokens of
  *             several layers can share one list)
  *   transpose:nonzero: the transposed map, i.e. the gradient with respect to x

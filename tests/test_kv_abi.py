@@ -86,7 +86,8 @@ SH = dict(L=2, S=3, H=4, cap=100, block_len=32, dtype="int8")
 @pytest.mark.parametrize("kw", [dict(L=0), dict(S=0), dict(H=-1), dict(cap=0), dict(cap=(1 << 26) + 1), dict(d=64),
                                 dict(block_len=0), dict(block_len=24), dict(block_len=1040), dict(block_len=-16),
                                 dict(dtype=milo.MILO_BF16), dict(dtype=milo.MILO_INT2), dict(dtype=77),
-                                dict(L=1 << 12, S=1 << 12, H=1 << 12)])
+                                dict(L=1 << 12, S=1 << 12, H=1 << 12),
+                                dict(L=1 << 10, S=1 << 10, H=1 << 10, cap=1 << 26)])
 def test_kv_shape_refused(L, kw):
     s = milo.kv_shape(**{**SH, **kw})
     assert milo.milo_kv_cache_size(s) == 0

@@ -269,6 +269,18 @@ def test_append_strides_of_a_packed_projection():
 
 
 @pytest.mark.parametrize("dtype", KINDS)
+def test_append_one_token_of_a_strided_view(dtype):
+    """A dimension of one index may have any stride."""
+    a, b = make(1, 2, 3, 32, 16, dtype), make(1, 2, 3, 32, 16, dtype)
+    x = rnd(50, 2, 2, 3, 130 * 8)[:, :, :, :128]
+    k, v = (x[i].as_strided((1, 2, 3, 1, 128), (7, 3 * 1040, 1040, 5, 1), x[i].storage_offset()) for i in (0, 1))
+    append(a, k, v, [0, 31])
+    append(b, k.contiguous(), v.contiguous(), [0, 31])
+    ok()
+    assert torch.equal(a.buf, b.buf)
+
+
+@pytest.mark.parametrize("dtype", KINDS)
 def test_append_bad_ranges_and_values(dtype):
     L, S, H, cap = 1, 5, 1, 40
     c = make(L, S, H, cap, 16, dtype)
@@ -363,6 +375,26 @@ def test_select(G, dt, bl, cap, n_q):
             np.testing.assert_array_equal(sc[l, s, i, h, :cand], ref[:cand])
             assert np.all(np.isneginf(sc[l, s, i, h, cand:]))
             np.testing.assert_array_equal(sel[l, s, i, h], R.top(ref, cand, n_sel, nf, nl))
+    ok()
+
+
+@pytest.mark.parametrize("n_b,n_sel,nf,nl", [(2500, 40, 2, 3), (2500, 2499, 0, 0), (9000, 100, 1, 1), (9000, 8500, 0, 0),
+                                             (9000, 2, 1, 1)])
+def test_select_many_blocks(n_b, n_sel, nf, nl):
+    """More blocks than a small CTA's registers hold, and than a large one's; many equal scores."""
+    cap = 16 * n_b
+    c = make(1, 1, 1, cap, 16, "int4")
+    k = rnd(14, 1, 1, 1, cap, 128)
+    k[:, :, :, 16 * 100:16 * 2200] = k[:, :, :, :16].repeat(1, 1, 1, 2100, 1)
+    append(c, k, k, [0])
+    q = rnd(15, 1, 1, 2, 128)
+    got, _ = sections(c)
+    for length in (cap, cap - 16 * 50 - 3):
+        sel, sc = milo.milo_kv_select(c, q, i32([length]), n_sel, nf, nl, return_scores=True)
+        cand = -(-length // 16)
+        ref = R.scores(f32np(q)[0, 0], got["codes"][0, 0, 0], got["scale"][0, 0, 0])
+        np.testing.assert_array_equal(sc.cpu().numpy()[0, 0, 0, :cand], ref[:cand])
+        np.testing.assert_array_equal(sel.cpu().numpy()[0, 0, 0], R.top(ref, cand, n_sel, nf, nl))
     ok()
 
 
@@ -497,7 +529,7 @@ def test_attn_many_query_rows_large_and_small_values(dtype, dt):
 
 @pytest.mark.parametrize("dtype", KINDS)
 @pytest.mark.parametrize("dt", [BF, F32])
-@pytest.mark.parametrize("bl,n_q,G", [(16, 1, 7), (48, 2, 3), (64, 1, 8), (128, 1, 12)])
+@pytest.mark.parametrize("bl,n_q,G", [(16, 1, 7), (48, 2, 3), (64, 1, 8), (128, 1, 12), (32, 1, 20)])
 def test_attn_selected_blocks(dtype, dt, bl, n_q, G):
     L, S, H, cap = 2, 4, 2, 700
     length = [700, 333, 1, 0]
@@ -710,6 +742,30 @@ def test_decode_over_compressed_blocks_and_cache(oracle_mod):
     n = L.milo_decode_kv_workspace_size(f.handle, S, w.Hq, sel.shape[1], ctypes.byref(c.shape), 0)
     args = args[:8] + (ctypes.byref(c.shape), c.buf.data_ptr(), c.buf.numel()) + args[11:]
     assert L.milo_decode_attn_kv(*args, n - 1, None) == milo.MILO_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+@pytest.mark.parametrize("G", [3, 12, 20])
+def test_decode_over_blocks_and_cache_by_group_size(dtype, G):
+    """Query groups of each attention kernel, more tokens than one CTA takes."""
+    w = synth.WORKLOADS["toy"]
+    K, V = synth.workload_cache(w)
+    f = milo.milo_compress(K.cuda(), V.cuda(), w.block_len, milo.default_params(factor_dtype="f32"))
+    S = 2
+    q = rnd(47, 1, S, G, 128)
+    sel = i32([[0, 3], [5, 1]])
+    c = make(1, S, 1, 5000, 64, dtype)
+    k, v = rnd(48, 1, S, 1, 5000, 128), rnd(49, 1, S, 1, 5000, 128)
+    append(c, k, v, [0] * S)
+    kt, vt = milo.milo_kv_read(c, i32([0] * S), 5000)
+    for length in ([5000, 17], [0, 1], [0, 0]):
+        want = milo.milo_decode_attn_tail(f, q, sel, kt, vt, i32(length))
+        got = milo.milo_decode_attn_kv(f, q, sel, c, i32(length))
+        # both in fp32 sums over 5000 tokens of size 1: their bounds in R.attn, a few 1e-4 of the largest value
+        assert float((got - want).abs().max()) <= 2e-4 * float(want.abs().max())
+        if length == [0, 0]:
+            assert torch.equal(got, milo.milo_decode_attn(f, q, sel))
+    ok()
 
 
 def test_stage_timing_counts_the_calls():
