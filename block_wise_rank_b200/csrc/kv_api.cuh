@@ -449,7 +449,7 @@ milo_status milo_kv_select(const milo_kv_shape *shape, const void *cache, size_t
     else k_kv_score<float><<<grid, 32 * KV_SCORE_WARPS, 0, s>>>(a, per);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess)
-        e = a.c.n_b <= 2048   ? kv_follow(k_kv_topn<256, 8, true>, dim3(rows), 256, a, s)
+        e = a.c.n_b <= 2048   ? kv_follow(k_kv_topn<512, 4, true>, dim3(rows), 512, a, s)
             : a.c.n_b <= 8192 ? kv_follow(k_kv_topn<1024, 8, true>, dim3(rows), 1024, a, s)
                               : kv_follow(k_kv_topn<1024, 1, false>, dim3(rows), 1024, a, s);
     tpush(MILO_TK_KV_SELECT, t0, tmark(s));

@@ -129,9 +129,6 @@ template <int DT> __device__ __forceinline__ int ka_chunk(int t, int c) {
 __device__ __forceinline__ void ka_copy16(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
-__device__ __forceinline__ void ka_copy16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void ka_copy4(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
 }
@@ -147,18 +144,6 @@ __device__ __forceinline__ void ka_fetch(uint32_t dst, const KaLine<DT> &ln, int
     const unsigned char *k = ln.k + ((int64_t)t0 * Tl::ROW + (r0 * Tl::ROW + 16 * c)), *v = k + (ln.v - ln.k);
     const unsigned char *p = (lane < 16 ? ln.kp : ln.vp) + ((int64_t)t0 * Tl::PAR + rp * Tl::PAR);
     const uint32_t top = dst + (lane < 16 ? Tl::KP : Tl::VP) + rp * Tl::PAR;
-    if (rem >= 16) {
-#pragma unroll
-        for (int i = 0; i < 16 / STEP; ++i) {
-            const int r = r0 + STEP * i;
-            const uint32_t to = dst + r * Tl::ROW + 16 * ka_chunk<DT>(r, c);
-            ka_copy16(to, k + STEP * i * Tl::ROW);
-            ka_copy16(to + Tl::V, v + STEP * i * Tl::ROW);
-        }
-        if (DT == MILO_INT4) ka_copy16(top, p);
-        else ka_copy4(top, p, true);
-        return;
-    }
 #pragma unroll
     for (int i = 0; i < 16 / STEP; ++i) {
         const int r = r0 + STEP * i;
