@@ -530,7 +530,7 @@ def milo_rope(x: torch.Tensor, positions: torch.Tensor, params: milo_rope_params
         raise ValueError(f"x: [n_tokens][n_heads][{params.d}] with contiguous rows expected, got {tuple(x.shape)}")
     s = _on(x, stream)
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        out = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
     elif out.shape != x.shape or (out.numel() and out.stride(2) != 1):
         raise ValueError(f"out: {tuple(x.shape)} with contiguous rows expected, got {tuple(out.shape)}")
     n_pos = positions.numel()
@@ -631,9 +631,9 @@ def milo_kv_read(cache: KvCache, start: torch.Tensor, n: int, count=None, k_out=
     c = cache.shape
     shape = (c.L, c.S, c.H, n, c.d)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=out_dtype, device=cache.buf.device)
+        k_out = cache.buf.new_empty(shape, dtype=out_dtype)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=k_out.dtype, device=cache.buf.device)
+        v_out = torch.empty_like(k_out)
     for t in (k_out, v_out):
         if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype != k_out.dtype:
             raise ValueError(f"k_out, v_out: contiguous {shape} of one type expected, got {t.dtype} {tuple(t.shape)}")
@@ -671,15 +671,15 @@ def milo_kv_select(cache: KvCache, q: torch.Tensor, length: torch.Tensor, n_sel:
     lead = (c.L, c.S, n_q, c.H) if q.dim() == 5 else (c.L, c.S, c.H)
     s = _on(q, stream)
     if selected is None:
-        selected = torch.empty(lead + (n_sel,), dtype=torch.int32, device=q.device)
+        selected = length.new_empty(lead + (n_sel,))
     _int32(selected, lead + (n_sel,), "selected")
     if scores is None and return_scores:
-        scores = torch.empty(lead + (cache.n_b,), dtype=torch.float32, device=q.device)
+        scores = q.new_empty(lead + (cache.n_b,), dtype=torch.float32)
     if scores is not None and (scores.dtype != torch.float32 or tuple(scores.shape) != lead + (cache.n_b,) or
                                not scores.is_contiguous()):
         raise ValueError(f"scores: contiguous float32 {lead + (cache.n_b,)} expected")
     if workspace is None:
-        workspace = _bytes(cache._ws("milo_kv_select_workspace_size", n_q), q.device)
+        workspace = cache.buf.new_empty(cache._ws("milo_kv_select_workspace_size", n_q))
     _same_device(q, length, selected, scores, workspace, cache.buf)
     rc = lib().milo_kv_select(c, cache.buf.data_ptr(), cache.buf.numel(), q.data_ptr(), _dtype_code(q.dtype), n_q, Hq,
                               length.data_ptr(), n_sel, n_first, n_last, selected.data_ptr(),
@@ -710,9 +710,9 @@ def milo_kv_attn(cache: KvCache, q: torch.Tensor, length: torch.Tensor, selected
         out = torch.empty_like(q)
     if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
         raise ValueError("out: like q expected")
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device) if return_lse else None
+    lse = q.new_empty(q.shape[:-1], dtype=torch.float32) if return_lse else None
     if workspace is None:
-        workspace = _bytes(cache._ws("milo_kv_attn_workspace_size", n_q, Hq, n_sel), q.device)
+        workspace = cache.buf.new_empty(cache._ws("milo_kv_attn_workspace_size", n_q, Hq, n_sel))
     _same_device(q, length, selected, out, workspace, cache.buf)
     rc = lib().milo_kv_attn(c, cache.buf.data_ptr(), cache.buf.numel(), q.data_ptr(), _dtype_code(q.dtype), n_q, Hq,
                             length.data_ptr(), None if selected is None else selected.data_ptr(), n_sel, scale,
