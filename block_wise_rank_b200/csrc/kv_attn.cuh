@@ -116,8 +116,17 @@ template <int DT> struct KaTile {
     static constexpr int STAGES = DT == MILO_INT4 ? 5 : 3;
 };
 
+// where a lane's share of row 0's tile comes from: chunks of keys and values, and one row's parameters
 template <int DT> struct KaLine {
-    const unsigned char *k, *v, *kp, *vp;
+    const unsigned char *k, *v, *p;
+    __device__ __forceinline__ KaLine(const unsigned char *k0, const unsigned char *v0, const unsigned char *kp,
+                                      const unsigned char *vp, int lane) {
+        constexpr int PER = KaTile<DT>::ROW / 16;
+        const int at = lane / PER * KaTile<DT>::ROW + 16 * (lane % PER);
+        k = k0 + at;
+        v = v0 + at;
+        p = (lane < 16 ? kp : vp) + (lane & 15) * KaTile<DT>::PAR;
+    }
 };
 
 template <int DT> __device__ __forceinline__ int ka_token(int r) { return DT == MILO_INT4 ? r ^ ((r >> 1) & 1) : r; }
@@ -141,8 +150,8 @@ __device__ __forceinline__ void ka_fetch(uint32_t dst, const KaLine<DT> &ln, int
     using Tl = KaTile<DT>;
     constexpr int PER = Tl::ROW / 16, STEP = 32 / PER;       // chunks of a row, rows per round of the warp
     const int c = lane % PER, r0 = lane / PER, rp = lane & 15;
-    const unsigned char *k = ln.k + ((int64_t)t0 * Tl::ROW + (r0 * Tl::ROW + 16 * c)), *v = k + (ln.v - ln.k);
-    const unsigned char *p = (lane < 16 ? ln.kp : ln.vp) + ((int64_t)t0 * Tl::PAR + rp * Tl::PAR);
+    const unsigned char *k = ln.k + (int64_t)t0 * Tl::ROW, *v = ln.v + (int64_t)t0 * Tl::ROW;
+    const unsigned char *p = ln.p + (int64_t)t0 * Tl::PAR;
     const uint32_t top = dst + (lane < 16 ? Tl::KP : Tl::VP) + rp * Tl::PAR;
 #pragma unroll
     for (int i = 0; i < 16 / STEP; ++i) {
@@ -348,13 +357,42 @@ template <bool SEL, int NT> struct KaRun {
     int64_t u0, u1, n_units, line0;    // n_units: of every CTA; line0: first unit of the line
     int k, per, l, h;                  // class, units of its lines, the line's layer and head
 
+    __device__ __forceinline__ bool mine_of(int64_t total) {
+        n_units = ka_div(total + gridDim.x - 1, gridDim.x);
+        u0 = blockIdx.x * n_units;
+        u1 = min(total, u0 + n_units);
+        return u0 < u1;
+    }
     // Finds the run (the whole CTA calls it); false if it is empty.
     __device__ __forceinline__ bool begin(const KvAttnArgs &a, KaScan &sc) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, LH = a.c.L * a.c.H;
-        int64_t total;
-        if (SEL) {
-            cl.set(a, 0, false);
-            total = (int64_t)a.classes * LH * cl.units(a);
+        int64_t total, cls0 = 0;
+        if (SEL) {   // every line has the same units
+            per = cl.units(a);
+            total = (int64_t)a.classes * LH * per;
+            if (!mine_of(total)) return false;
+            const int64_t w = (int64_t)per * LH;
+            k = (int)ka_div(u0, w);
+            cls0 = k * w;
+            cl.set(a, k, tid == 0);
+        } else if (a.classes <= 32) {   // a class a lane, each warp for itself: no barrier
+            KaClass<SEL, NT> at;
+            int64_t mine = 0;
+            if (lane < a.classes) {
+                at.set(a, lane, blockIdx.x == 0 && warp == 0);
+                mine = (int64_t)at.units(a) * LH;
+            }
+            int64_t inc = mine;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += x;
+            }
+            total = __shfl_sync(0xffffffffu, inc, 31);
+            if (!mine_of(total)) return false;
+            k = __popc(__ballot_sync(0xffffffffu, inc <= u0));   // the classes that end before u0
+            cls0 = __shfl_sync(0xffffffffu, inc - mine, k);
+            cl.set(a, k, false);
+            per = cl.units(a);
         } else {
             const int chunk = (a.classes + THREADS - 1) / THREADS;
             const int k0 = (int)min((int64_t)a.classes, (int64_t)tid * chunk), k1 = min(a.classes - k0, chunk) + k0;
@@ -390,22 +428,12 @@ template <bool SEL, int NT> struct KaRun {
                 sc.off = at;
             }
             __syncthreads();
-        }
-        n_units = ka_div(total + gridDim.x - 1, gridDim.x);
-        u0 = blockIdx.x * n_units;
-        u1 = min(total, u0 + n_units);
-        if (u0 >= u1) return false;
-        int64_t cls0;
-        if (SEL) {
-            const int64_t w = (int64_t)cl.units(a) * LH;
-            k = (int)ka_div(u0, w);
-            cls0 = k * w;
-        } else {
+            if (!mine_of(total)) return false;
             k = sc.cls;
             cls0 = sc.off;
+            cl.set(a, k, false);
+            per = cl.units(a);
         }
-        cl.set(a, k, SEL && tid == 0);
-        per = cl.units(a);
         const int lh = (int)ka_div(u0 - cls0, per);
         line0 = cls0 + (int64_t)lh * per;
         l = lh / a.c.H;
@@ -490,8 +518,20 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
     while (run.u0 < run.u1) {
         const int s0 = run.s0(), s1 = run.s1(), l = run.l, h = run.h;
         const int64_t sh = (int64_t)cl.s * a.c.H + h;
-        const KaLine<DT> ln{a.c.codes(l, sh, 0), a.c.codes(l, sh, 1), a.c.params(l, sh, 0), a.c.params(l, sh, 1)};
+        const KaLine<DT> ln(a.c.codes(l, sh, 0), a.c.codes(l, sh, 1), a.c.params(l, sh, 0), a.c.params(l, sh, 1), lane);
         const int32_t *sel = SEL ? a.sel + ((((int64_t)l * a.c.S + cl.s) * a.n_q + cl.i) * a.c.H + h) * a.n_sel : nullptr;
+        // the line's queries, a warp per row (RPT / KA_WARPS rows each): asked for before the codes
+        float qx[RPT / KA_WARPS][4];
+#pragma unroll
+        for (int y = 0; y < RPT / KA_WARPS; ++y) {
+            const int r = warp + y * KA_WARPS;
+            const T *q = (const T *)a.q + cl.row(a, l, h, min(r, cl.rows - 1)) * D + 4 * lane;
+            T t[4];                                          // 16 or 8 bytes
+            if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(t) = __ldg(reinterpret_cast<const uint4 *>(q));
+            else *reinterpret_cast<uint2 *>(t) = __ldg(reinterpret_cast<const uint2 *>(q));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) qx[y][e] = r < cl.rows ? to_f32(t[e]) : 0.f;
+        }
         // the segment's tiles, an equal run of them to each warp: `left` of them, fetched a few ahead of their use
         const int first = max(s0 - KA_BEGIN, 0) * KA_WARPS;
         const int tiles = max(min(cl.tiles(a), (s1 - KA_BEGIN) * KA_WARPS) - first, 0);
@@ -538,17 +578,6 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
         for (int i = 0; i < AHEAD; ++i) fetch(i);
 
         // the line's queries as fragments, a warp per row (RPT / KA_WARPS rows each)
-        float qx[RPT / KA_WARPS][4];
-#pragma unroll
-        for (int y = 0; y < RPT / KA_WARPS; ++y) {
-            const int r = warp + y * KA_WARPS;
-            const T *q = (const T *)a.q + cl.row(a, l, h, min(r, cl.rows - 1)) * D + 4 * lane;
-            T t[4];                                          // 16 or 8 bytes
-            if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4 *>(t) = __ldg(reinterpret_cast<const uint4 *>(q));
-            else *reinterpret_cast<uint2 *>(t) = __ldg(reinterpret_cast<const uint2 *>(q));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) qx[y][e] = r < cl.rows ? to_f32(t[e]) : 0.f;
-        }
 #pragma unroll
         for (int y = 0; y < RPT / KA_WARPS; ++y) {
             const int r = warp + y * KA_WARPS;
