@@ -117,8 +117,8 @@ milo_status kv_query_check(const milo_kv_shape *s, const void *q, milo_dtype q_d
     return MILO_OK;
 }
 
-// grid size for `ctas` thread blocks in x, 0 if there are too many
-unsigned grid_x(int64_t ctas) { return ctas > INT32_MAX ? 0u : (unsigned)ctas; }
+// grid size for `ctas` thread blocks in x, 0 if there are too many (2^30, so that four items a block still count in 32 bits)
+unsigned grid_x(int64_t ctas) { return ctas > (1 << 30) ? 0u : (unsigned)ctas; }
 
 template <typename T, int DT> void kv_append_run(const KvAppendArgs &a, cudaStream_t s) {
     // a warp to an item where a step takes all its tokens, or where the items fill the GPU (16 warps an SM) twice over:
@@ -329,6 +329,7 @@ milo_status milo_rope(const milo_rope_params *p, const void *x, milo_dtype x_dty
     a.n_hc = (n_heads + a.hpt - 1) / a.hpt;
     a.hpt = (n_heads + a.n_hc - 1) / a.n_hc;   // equal chunks
     if (grid_x((per_head * a.n_hc + 255) / 256) == 0) return MILO_ERR_UNSUPPORTED;
+    a.small = per_head * a.n_hc + 255 < (int64_t(1) << 32);
     cudaStream_t s = (cudaStream_t)stream;
     cudaEvent_t t0 = tmark(s);
     auto go = [&](auto tx, auto ty) {
@@ -438,6 +439,7 @@ milo_status milo_kv_select(const milo_kv_shape *shape, const void *cache, size_t
     a.q = q; a.len = len; a.selected = selected; a.scores = scores ? scores : (float *)workspace;
     a.n_q = n_q; a.G = Hq / shape->H; a.n_sel = n_sel; a.n_first = n_first; a.n_last = n_last;
     const unsigned rows = grid_x((int64_t)shape->L * shape->S * n_q * shape->H);
+    if (!rows) return MILO_ERR_UNSUPPORTED;
     // blocks per CTA: as many steps of its warps as leave one wave of four CTAs an SM (a CTA first codes its queries, about
     // what two steps cost)
     const int64_t steps = (a.c.n_b + KV_SCORE_STEP - 1) / KV_SCORE_STEP, wave = 4 * sm_count();

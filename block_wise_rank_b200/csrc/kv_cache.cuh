@@ -4,6 +4,11 @@
 // The layout and the arithmetic of the codes are milo.h's (milo_kv_shape).
 // Every code is decided by IEEE fp32 operations on the stored parameters, the
 // bounds by minima and maxima, so nothing depends on the order of the work.
+//
+// Writing is bound by instructions (16 channels take about 240, 64 of them the exact
+// quotients) a little before memory: 106496 bf16 rows of 4 heads into e4m3
+// in 76 us, 4.4 TB/s (with the division's subroutine 173 us).  Reading is bound
+// by memory: the same rows back to bf16 in 53 us, 6.2 TB/s.
 #pragma once
 #include <cuda_fp8.h>
 

@@ -7,6 +7,12 @@
 //   sum_j min(c_j, 0) lo_j + max(c_j, 0) hi_j,
 // one dot product of 256 8-bit values, exact in integers whatever the order,
 // so that equal blocks tie and every run picks the same ones.
+//
+// Measured on 32 sessions of 30000 to 131072 tokens, 4 KV heads of 7 query heads,
+// blocks of 64: 23 us for both kernels.  The scores take about 14 of them for 42 MB
+// (6.6 us at the copy rate): the lengths differ, so CTAs of one wave end apart, and each
+// first codes its queries.  The selection is a chain of short rounds, 6 to 9 us however
+// few the rows are.
 #pragma once
 #include "kv_cache.cuh"
 

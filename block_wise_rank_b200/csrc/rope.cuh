@@ -9,7 +9,10 @@
 // Bound by memory: each row is read and written once.  A thread owns one unit
 // of V pairs (or V copied channels) of one token and walks a chunk of the
 // heads, so a token's angles are computed once per chunk and stay in
-// registers.
+// registers; the loads of several heads are issued together (128 bytes a
+// thread).  Measured on 32768 tokens x 32 heads x 128 bf16: 90 us, 5.9 TB/s,
+// 90 % of the measured copy rate (one head at a time 120 us, two 111 us); 28 tokens
+// of a decode step, 3 us in a graph.
 #pragma once
 #include "project_simt.cuh"   // from_f32
 
@@ -25,6 +28,7 @@ struct RopeArgs {
     int d, rd, heads;
     int hpt, n_hc;                       // heads per thread, chunks of heads
     int units, rot_units;                // units of a row, those that turn
+    bool small;                          // the launch has fewer than 2^32 threads
     float m;                             // factor on the turned channels
     float sgn;                           // -1: transposed
 };
@@ -85,11 +89,20 @@ template <typename T, int V> __device__ __forceinline__ void rope_store(T *p, co
 // pairs); otherwise V pairs (i, i + rd / 2), i.e. two accesses.
 template <typename TX, typename TY, int V, bool INTER>
 __global__ void __launch_bounds__(256, 3) k_rope(const __grid_constant__ RopeArgs a) {
-    const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    const int u = (int)(gid % a.units);
-    const int64_t r = gid / a.units;
-    const int hc = (int)(r % a.n_hc);
-    const int64_t t = r / a.n_hc;
+    int u, hc;
+    int64_t t;
+    if (a.small) {   // fewer than 2^32 threads: 64-bit divisions would take as long as a small call's transfer
+        const uint32_t gid = blockIdx.x * blockDim.x + threadIdx.x, r = gid / (uint32_t)a.units;
+        u = (int)(gid - r * (uint32_t)a.units);
+        const uint32_t q = r / (uint32_t)a.n_hc;
+        hc = (int)(r - q * (uint32_t)a.n_hc);
+        t = q;
+    } else {
+        const int64_t gid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, r = gid / a.units;
+        u = (int)(gid % a.units);
+        hc = (int)(r % a.n_hc);
+        t = r / a.n_hc;
+    }
     if (t >= a.n_tokens) return;
     const int h0 = hc * a.hpt, h1 = min(a.heads, h0 + a.hpt);
     const TX *x = (const TX *)a.x + t * a.xt;
@@ -108,7 +121,7 @@ __global__ void __launch_bounds__(256, 3) k_rope(const __grid_constant__ RopeArg
     constexpr int NP = INTER ? (V + 1) / 2 : V;   // pairs of a unit
     // heads whose loads are issued together: up to 128 bytes in flight a thread
     constexpr int FIT = 128 / (V * (int)sizeof(TX) * (INTER ? 1 : 2)), ROPE_HEADS = FIT < 4 ? FIT : 4;
-    const double p = (double)a.pos[t % a.n_pos];
+    const double p = (double)a.pos[a.n_pos >= a.n_tokens ? t : t % a.n_pos];
     float cs[NP], sn[NP];
     const int i0 = u * NP;
 #pragma unroll
