@@ -650,6 +650,13 @@ def milo_kv_read(cache: KvCache, start: torch.Tensor, n: int, count=None, k_out=
     return k_out, v_out
 
 
+def _kv_listed(selected: torch.Tensor) -> int:
+    """Blocks of a selection; an empty one would be taken for none, which stands for every token."""
+    if selected.dim() == 0 or selected.shape[-1] == 0:
+        raise ValueError("a selection of at least one block id expected (-1 for none)")
+    return selected.shape[-1]
+
+
 def _kv_queries(cache: KvCache, q: torch.Tensor, length: torch.Tensor):
     """(n_q, Hq) of q [L][S][n_q][Hq][d] or [L][S][Hq][d]."""
     c = cache.shape
@@ -701,10 +708,9 @@ def milo_kv_attn(cache: KvCache, q: torch.Tensor, length: torch.Tensor, selected
     [L][S](n_q)[H][n_sel]; with return_lse also the fp32 log-sum-exp."""
     c = cache.shape
     n_q, Hq = _kv_queries(cache, q, length)
+    n_sel = 0 if selected is None else _kv_listed(selected)
     s = _on(q, stream)
-    n_sel = 0
     if selected is not None:
-        n_sel = selected.shape[-1]
         _int32(selected, tuple(q.shape[:-2]) + (c.H, n_sel), "selected")
     if out is None:
         out = torch.empty_like(q)
@@ -732,13 +738,12 @@ def milo_decode_attn_kv(f: Factors, q: torch.Tensor, selected: torch.Tensor, cac
     if q.dtype != torch.float32 or q.dim() != 4:
         raise ValueError("q: float32 [L][S][Hq][d] expected")
     _, Hq = _kv_queries(cache, q, length)
+    kv_n_sel = 0 if kv_selected is None else _kv_listed(kv_selected)
     s = _on(q, stream)
     _int32(selected, (c.S, selected.shape[-1]), "selected")
     if positions is not None:
         _int32(positions, selected.shape, "positions")
-    kv_n_sel = 0
     if kv_selected is not None:
-        kv_n_sel = kv_selected.shape[-1]
         _int32(kv_selected, (c.L, c.S, c.H, kv_n_sel), "kv_selected")
     if out is None:
         out = torch.empty_like(q)

@@ -194,6 +194,15 @@ def test_binding_refuses_tensors(L):
         milo.milo_kv_select(c, z(2, 3, 8, 128), z(4, dt=torch.int32), 1)
 
 
+def test_binding_refuses_an_empty_selection(L):
+    c = milo.KvCache(milo.kv_shape(**SH), device="cpu")
+    q, i, none = torch.zeros(2, 3, 8, 128), torch.zeros(3, dtype=torch.int32), torch.zeros(2, 3, 4, 0, dtype=torch.int32)
+    with pytest.raises(ValueError, match="at least one block"):
+        milo.milo_kv_attn(c, q, i, none)
+    with pytest.raises(ValueError, match="at least one block"):
+        milo.milo_decode_attn_kv(None, q, none, c, i, none)
+
+
 # ------------------------------------------------ the reference's own pins
 def test_reference_codes():
     g = torch.Generator().manual_seed(1)
