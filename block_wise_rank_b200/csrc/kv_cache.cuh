@@ -18,7 +18,9 @@ namespace milo {
 
 constexpr int KV_GROUP = 32;                 // channels that share an INT4 scale and zero
 constexpr int KV_NG = D / KV_GROUP;
-constexpr float KV_F16_MAX = 65504.f;
+// Greatest INT4 value: a group's highest value 15 s + z passes its maximum by 60 + 16 at most, the roundings of s
+// (at most 8725) and z, and has to stay below 65520, which rounds past fp16's end
+constexpr float KV_INT4_MAX = 65440.f;
 
 // One layer-strided cache buffer.
 struct KvView {
@@ -240,7 +242,7 @@ template <> struct KvBounds<__nv_bfloat16> {   // two channels an instruction
             hi[i] = __hmax2(hi[i], v[i]);
         }
     }
-    __device__ __forceinline__ void add(const float (&x)[16]) {   // x are bf16 values (or +-65504, which rounds outward)
+    __device__ __forceinline__ void add(const float (&x)[16]) {   // x are bf16 values (or +-65440, which rounds outward)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
@@ -318,13 +320,13 @@ __global__ void __launch_bounds__(32 * KV_APPEND_WARPS, sizeof(T) == 4 ? 5 : 6) 
         kv_f32<T>(raw, r);
         if (t + 4 * WPI < t1) next = kv_raw16<T>(x + (int64_t)(t + 4 * WPI) * a.st);
         uint32_t top = kv_top<T>(raw);
-        if (live && top > __float_as_uint(DT == MILO_INT4 ? KV_F16_MAX : 3.402823466e38f)) {
+        if (live && top > __float_as_uint(DT == MILO_INT4 ? KV_INT4_MAX : 3.402823466e38f)) {
             bad = true;
             top = 0u;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 if (!isfinite(r[i])) r[i] = 0.f;
-                if (DT == MILO_INT4 && fabsf(r[i]) > KV_F16_MAX) r[i] = copysignf(KV_F16_MAX, r[i]);
+                if (DT == MILO_INT4 && fabsf(r[i]) > KV_INT4_MAX) r[i] = copysignf(KV_INT4_MAX, r[i]);
                 top = max(top, __float_as_uint(r[i]) & 0x7fffffffu);
             }
             if (kind == 0) bounds.add(r);

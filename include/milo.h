@@ -454,7 +454,8 @@ typedef struct {
  *   5  bcodes   [S][H][n_b][2][128]   int8 codes of the bounds
  *   6  bscale   [S][H][n_b]           float scale of the codes
  * A row x of 128 values is held as
- *   INT8  s = max|x| / 127, code = rint(x / s), value = code * s
+ *   INT8  s = max|x| / 127, code = rint(x / s), value = code * s (infinite for
+ *         an x that is within a place of the largest fp32)
  *   FP8   s = max|x| / 448, code = e4m3(x / s), value = code * s
  *   INT4  per group of 32 channels z = fp16(min), s = fp16((max - min) / 15),
  *         code = clamp(rint((x - z) / s), 0, 15), value = fp16(code * s + z);
@@ -482,8 +483,9 @@ milo_status milo_kv_layout(const milo_kv_shape *shape, size_t *offsets);
  *             tokens are written; NULL = n_new
  * A range outside [0, cap] (or a bad count) sets MILO_ERR_BOUNDS and that
  * session's rows are left as they were.  Rows outside the ranges are never
- * touched.  A value that is not finite (MILO_INT4: above 65504 in size) sets
- * MILO_ERR_NONFINITE and is stored as 0 (as +-65504).
+ * touched.  A value that is not finite (MILO_INT4: above 65440 in size, so
+ * that every fp16 value of a group is finite) sets MILO_ERR_NONFINITE and is
+ * stored as 0 (as +-65440).
  * The bounds of a block whose first token is written are those of the written
  * tokens; a block that is continued keeps what it had (rows written again
  * widen its bounds, never narrow them), so a session begins at token 0.

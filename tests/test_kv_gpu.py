@@ -130,6 +130,18 @@ def test_rope_positions_repeat_over_layers():
     check_rope(x, pos, milo.milo_rope(x, i32(pos), p), p, R.rope_freqs(128, 1e6))
 
 
+def test_rope_more_than_2_to_32_threads():
+    """One row for 2^32 + 5 tokens: indices that 32 bits do not hold."""
+    n, p = 2 ** 32 + 5, milo.rope_params(2)
+    x, pos = rnd(41, 1, 1, 2, dtype=BF), i32([12345])
+    want = milo.milo_rope(x, pos, p).view(torch.int32).item()
+    y = milo.milo_rope(x.expand(n, 1, 2), pos, p)
+    assert y.shape == (n, 1, 2) and not (y.view(torch.int32) != want).any()
+    ok()
+    del y
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_rope_gradient(inter):
     """Against the formula (the transposed map) and against differences of the forward pass."""
@@ -319,6 +331,30 @@ def test_append_smallest_and_largest_values():
     np.testing.assert_array_equal(got["k"][:, :, :, :4], q)
     np.testing.assert_array_equal(got["kp"][:, :, :, :4], p)
     assert np.isfinite(got["bounds"][0, 0, 0, 0]).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_int4_values_of_the_widest_groups_are_finite(dt):
+    """Groups that span fp16: the highest code's value must not round past its end."""
+    n = 64
+    x = rnd(51, 1, 1, 1, n, 128, dtype=dt)
+    x[..., 0::32] = 65504.0 if dt == F32 else 65280.0            # bf16 above 65280 is 65536
+    x[..., 1::32] = -65504.0 if dt == F32 else -65280.0
+    low = -40336.0 + 16 * torch.arange(n // 2, device="cuda")     # zeros that are rounded up by half a step
+    x[..., :n // 2, 1::32] = low.to(dt)[:, None]
+    c = make(1, 1, 1, n, 16, "int4")
+    append(c, x, x, [0])
+    ok(milo.MILO_ERR_NONFINITE if dt == F32 else milo.MILO_OK)
+    z = f32np(x.clamp(-65440, 65440) if dt == F32 else x)
+    q, p = R.quantise(z, "int4")
+    got, _ = sections(c)
+    np.testing.assert_array_equal(got["k"], q)
+    np.testing.assert_array_equal(got["kp"], p)
+    k, v = milo.milo_kv_read(c, i32([0]), n)
+    assert torch.isfinite(k).all() and torch.equal(k, v)
+    np.testing.assert_array_equal(f32np(k), R.values(q, p, "int4").astype(np.float32))
+    for n_q in (1, 40):                                          # both attention kernels
+        check_attn(c, rnd(52, 1, 1, n_q, 2, 128, scale=1e-6), [n])
 
 
 @pytest.mark.parametrize("dtype", KINDS)
@@ -621,6 +657,44 @@ def test_attn_writes_only_its_output():
 
 
 # ------------------------------------------------- as they are used together
+def test_rows_behind_4_gigabytes():
+    """A session whose last rows lie behind 2^32 bytes: written, read, picked and attended."""
+    H, cap, bl, n = 2, 2 ** 25 + 4099, 1024, 50
+    c = make(1, 1, H, cap, bl, "int8", fill=0)                   # zero rows: score 0, value 0
+    k, v = rnd(53, 1, 1, H, n, 128), rnd(54, 1, 1, H, n, 128)
+    append(c, k, v, [cap - n])
+    ko, vo = milo.milo_kv_read(c, i32([cap - n]), n)
+    kr, vr = (R.values(*R.quantise(f32np(x), "int8"), "int8") for x in (k, v))
+    assert np.array_equal(f32np(ko), kr.astype(np.float32)) and np.array_equal(f32np(vo), vr.astype(np.float32))
+    q = (2 * k[:, :, :, -1]).contiguous()                        # [1][1][Hq = H][128]
+    sel = milo.milo_kv_select(c, q, i32([cap]), 2, 0, 0)
+    assert sel.cpu().numpy().tolist() == [[[[c.n_b - 2, c.n_b - 1]] * H]]
+    for picked in (None, sel):
+        o, lse = milo.milo_kv_attn(c, q, i32([cap]), picked, return_lse=True)
+        ok()
+        zeros = (cap if picked is None else bl + cap % bl) - n     # the rows lie in the last two blocks
+        for h in range(H):
+            qn = np64(q)[0, 0, h]
+            s = kr[0, 0, h] @ qn * 128 ** -0.5
+            w = np.exp(s)
+            total = w.sum() + zeros
+            # roundings as R.attn counts them; a thread adds at most cap / 16 / 1184 * 2 < 4096 weights, the parts are fewer
+            rel = 2.0 ** -23 * (28 * (np.abs(kr[0, 0, h]) @ np.abs(qn)) * 128 ** -0.5 + np.abs(s)) + 2.0 ** -21 + 2.0 ** -11
+            ref = w @ vr[0, 0, h] / total
+            tol = (w * rel) @ np.abs(vr[0, 0, h]) / total + rel.max() * np.abs(ref) + 2.0 ** -34 * np.abs(vr).max()
+            assert np.all(np.abs(np64(o)[0, 0, h] - ref) <= tol)
+            assert abs(np64(lse)[0, 0, h] - np.log(total)) <= rel.max() + 2.0 ** -23 * (1 + np.log(total))
+    del c
+    torch.cuda.empty_cache()
+
+
+def test_attn_refuses_an_empty_selection():
+    """No ids would be taken for no selection, which stands for every token."""
+    c, q = filled(1, 1, 1, 32, 16, "int8", [32]), rnd(55, 1, 1, 2, 128)
+    with pytest.raises(ValueError, match="at least one block"):
+        milo.milo_kv_attn(c, q, i32([32]), torch.empty(1, 1, 1, 0, dtype=torch.int32, device="cuda"))
+
+
 def test_one_layer_of_a_cache_is_a_cache():
     L, S, H = 3, 2, 2
     a, b = make(L, S, H, 50, 16, "int4"), make(L, S, H, 50, 16, "int4")
