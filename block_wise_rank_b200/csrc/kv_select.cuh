@@ -10,9 +10,10 @@
 //
 // Measured on 32 sessions of 30000 to 131072 tokens, 4 KV heads of 7 query heads,
 // blocks of 64: 23 us for both kernels.  The scores take about 14 of them for 42 MB
-// (6.6 us at the copy rate): the lengths differ, so CTAs of one wave end apart, and each
-// first codes its queries.  The selection is a chain of short rounds, 6 to 9 us however
-// few the rows are.
+// (6.6 us at the copy rate): a CTA is a chain of latencies, its length, its queries'
+// coding and then up to seven steps of one batch of loads (two batches in flight cost
+// registers, 25 us in all; equal runs of steps by the lengths begin more rows, 24 us).  The
+// selection is a chain of short rounds, 6 to 9 us however few the rows are.
 #pragma once
 #include "kv_cache.cuh"
 
