@@ -144,6 +144,7 @@ template <typename T> void kv_read_launch(const KvReadArgs &a, dim3 grid, cudaSt
 // Query rows of a line and the launch shape of an attention call.
 struct KvAttnPlan {
     int nt, row_tiles, grid, classes;
+    bool whole;
     size_t part_o, part_ml, split, bytes;    // workspace offsets
 };
 
@@ -161,8 +162,15 @@ KvAttnPlan kv_attn_plan(const milo_kv_shape *s, int32_t n_q, int32_t Hq, int32_t
     const int begin = p.nt == 1 ? KaShape<1>::BEGIN : p.nt == 2 ? KaShape<2>::BEGIN : KaShape<16>::BEGIN;
     const int ctas = p.nt == 1 ? KaShape<1>::CTAS : p.nt == 2 ? KaShape<2>::CTAS : KaShape<16>::CTAS;
     const int64_t tiles = n_sel ? (int64_t)n_sel * (s->block_len / 16) : ((int64_t)s->cap + 15) / 16;
-    const int64_t units = (int64_t)p.classes * s->L * s->H * (begin + (tiles + warps - 1) / warps);
-    p.grid = (int)std::min<int64_t>(units, ctas * sm_count());
+    const int64_t lines = (int64_t)p.classes * s->L * s->H, behind = (tiles + warps - 1) / warps;
+    const int most = p.nt == 1 ? KaShape<1>::WHOLE : p.nt == 2 ? KaShape<2>::WHOLE : KaShape<16>::WHOLE;
+    // short lines, no more than a wave holds: a CTA for each, one launch and nothing to merge; twice as long ones where
+    // they fill a quarter of the wave.  INT8, 7 bf16 heads a KV head, split against whole: 128 lines of 1000 tokens 19.0
+    // and 12.3 us, of 2000 24.6 and 18.5, 256 of 2000 36.6 and 28.8; 4 of 400 11.0 and 8.3, 2 of 1024 10.8 and 12.3;
+    // one of 2048 among 255 of 100 16.4 and 18.5; 256 of 4000 and more as fast or faster split
+    const int wave = ctas * sm_count();
+    p.whole = lines <= wave && behind <= (4 * lines >= wave ? 2 * most : most);
+    p.grid = (int)(p.whole ? lines : std::min<int64_t>(lines * (begin + behind), wave));
     p.part_o = 0;
     p.part_ml = align_up(sizeof(float) * 2 * (size_t)p.grid * rpt * D);
     p.split = p.part_ml + align_up(sizeof(float2) * 2 * (size_t)p.grid * rpt);
@@ -196,7 +204,7 @@ template <typename K> cudaError_t kv_smem(K kernel, size_t bytes, bool (&done)[6
 
 template <typename T, int NT, bool SEL> cudaError_t kv_attn_merge(const KvAttnArgs &a, int grid, cudaStream_t s) {
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || grid == 1) return e;
+    if (e != cudaSuccess || a.whole) return e;
     // many parts a line: a CTA per row, else one for 16 rows at most
     const int64_t lines = (int64_t)a.classes * a.c.L * a.c.H;
     const int rows = grid >= 16 * lines ? 8 * NT : (8 * NT + 15) / 16;
@@ -242,7 +250,7 @@ milo_status kv_attn_launch(const milo_kv_shape *shape, const void *cache, const 
     a.q = q; a.out = out; a.lse = lse; a.ml = ml; a.len = len; a.sel = selected;
     a.n_q = n_q; a.G = Hq / shape->H; a.n_sel = n_sel;
     a.tpb = shape->block_len / 16;
-    a.row_tiles = p.row_tiles; a.classes = p.classes;
+    a.row_tiles = p.row_tiles; a.classes = p.classes; a.whole = p.whole;
     a.scale = (float)((scale > 0.0 ? scale : 1.0 / std::sqrt((double)D)) * 1.4426950408889634074);
     a.part_o = (float *)((char *)workspace + p.part_o);
     a.part_ml = (float2 *)((char *)workspace + p.part_ml);

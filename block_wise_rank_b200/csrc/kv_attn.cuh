@@ -28,7 +28,8 @@
 // The (layer, session, KV head, query tile) lines are cut into units of 16 * WARPS
 // tokens, and every CTA of a single wave takes an equal run of units, whatever the
 // lengths are: a run that covers a line writes its result, the parts of a line that
-// several CTAs share are merged by k_kv_attn_merge in a fixed order.
+// several CTAs share are merged by k_kv_attn_merge in a fixed order.  Short lines
+// that one wave holds are not split, and there is no merge (kv_attn_plan).
 //
 // Measured: 8 sessions of 1000 to 131072 tokens, 4 KV heads of 7 bf16 query heads,
 // INT8: 104 us for 558 MB, 82 % of the measured copy rate (the kernel alone 93 us; codes
@@ -54,6 +55,7 @@ struct KvAttnArgs {
     int tpb;                       // tiles of 16 tokens per block
     int row_tiles;                 // query tiles of a line's rows
     int classes;                   // S * row_tiles (dense), S * n_q * row_tiles (selected)
+    bool whole;                    // a CTA for each line, and no parts to be merged
     float scale;                   // softmax scale * log2(e)
     float *part_o;                 // [2 grid][8 NT][D] normalised outputs of parts
     float2 *part_ml;               // [2 grid][8 NT] (reference, sum) of parts, in powers of two
@@ -65,6 +67,7 @@ struct KvAttnArgs {
 template <int NT> struct KaShape {
     static constexpr int WARPS = NT == 2 ? 4 : 8, CTAS = NT == 1 ? 2 : NT == 2 ? 3 : 1;   // warps of a CTA, CTAs of an SM
     static constexpr int BEGIN = NT == 1 ? 1 : 2;   // units that beginning and ending a line costs, counted at its front
+    static constexpr int WHOLE = NT == 16 ? 1 : 8;  // units behind them up to which few lines are not split
 };
 constexpr uint32_t KA_E_MIN = 0x08800000u;   // 2^-110: least 2^E, so that 2^(10 - E) is finite
 constexpr float KA_RAISE = 4.f;        // a score this far above the reference raises it
@@ -376,6 +379,17 @@ template <bool SEL, int NT> struct KaRun {
     __device__ __forceinline__ bool begin(const KvAttnArgs &a, KaScan &sc) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, LH = a.c.L * a.c.H;
         int64_t total, cls0 = 0;
+        if (!SEL && a.whole) {   // selected lines have equal units: their runs are whole lines by themselves
+            const int lh = blockIdx.x % LH;
+            k = blockIdx.x / LH;
+            l = lh / a.c.H;
+            h = lh - l * a.c.H;
+            cl.set(a, k, tid == 0 && lh == 0);
+            per = cl.units(a);
+            u0 = line0 = 0;
+            u1 = per;
+            return true;
+        }
         if (SEL) {   // every line has the same units
             per = cl.units(a);
             total = (int64_t)a.classes * LH * per;

@@ -539,6 +539,21 @@ def test_attn_many_query_rows(dtype, dt, n_q, G, H):
 
 @pytest.mark.parametrize("dtype", KINDS)
 @pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("cap,n_q,G", [(5000, 1, 7), (5000, 1, 12), (5000, 2, 3), (5000, 40, 4), (2048, 1, 8), (1024, 1, 12), (128, 9, 5)])
+def test_attn_short_lengths_of_long_and_short_caches(cap, dtype, dt, n_q, G):
+    """The same lengths where lines may be split over CTAs, and where a CTA takes a whole one."""
+    length = [0, 1, 15, 16, 17, 64, 127, 128, 100, 3, 128, 0]
+    for S in (2, 12):                                            # few lines and many
+        c = filled(1, S, 4, cap, 64, dtype, length[-S:])
+        q = rnd(56, 1, S, n_q, 4 * G, 128, dtype=dt)
+        check_attn(c, q, length[-S:])
+        sel = np.random.default_rng(cap).integers(-1, c.n_b, (1, S, n_q, 4, min(40, c.n_b))).astype(np.int32)
+        sel[..., :2] = [1, 0]
+        check_attn(c, q, length[-S:], sel.tolist())
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+@pytest.mark.parametrize("dt", [BF, F32])
 def test_attn_many_query_rows_large_and_small_values(dtype, dt):
     """The references and the value scales rise along the tiles: the output is rescaled."""
     L, S, H, n, n_q = 1, 2, 1, 900, 24
