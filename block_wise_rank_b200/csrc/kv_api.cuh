@@ -448,20 +448,32 @@ milo_status milo_kv_select(const milo_kv_shape *shape, const void *cache, size_t
     a.n_q = n_q; a.G = Hq / shape->H; a.n_sel = n_sel; a.n_first = n_first; a.n_last = n_last;
     const unsigned rows = grid_x((int64_t)shape->L * shape->S * n_q * shape->H);
     if (!rows) return MILO_ERR_UNSUPPORTED;
-    // blocks per CTA: as many steps of its warps as leave one wave of four CTAs an SM (a CTA first codes its queries, about
-    // what two steps cost)
-    const int64_t steps = (a.c.n_b + KV_SCORE_STEP - 1) / KV_SCORE_STEP, wave = 4 * sm_count();
-    const int per = KV_SCORE_STEP * (int)std::min<int64_t>((rows * steps + wave - 1) / wave, steps);
-    const dim3 grid(rows, (unsigned)((a.c.n_b + per - 1) / per));
     cudaStream_t s = (cudaStream_t)stream;
     cudaEvent_t t0 = tmark(s);
-    if (q_dtype == MILO_BF16) k_kv_score<__nv_bfloat16><<<grid, 32 * KV_SCORE_WARPS, 0, s>>>(a, per);
-    else k_kv_score<float><<<grid, 32 * KV_SCORE_WARPS, 0, s>>>(a, per);
-    cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess)
-        e = a.c.n_b <= 2048   ? kv_follow(k_kv_topn<512, 4, true>, dim3(rows), 512, a, s)
-            : a.c.n_b <= 8192 ? kv_follow(k_kv_topn<1024, 8, true>, dim3(rows), 1024, a, s)
-                              : kv_follow(k_kv_topn<1024, 1, false>, dim3(rows), 1024, a, s);
+    cudaError_t e;
+    // a CTA for each row and one launch, where the rows fill most of the SMs, or where they are short and read once (two
+    // launches against one, 7 bf16 heads unless said): 128 rows of 512 blocks 17.0 and 12.3 us, of 1024 19.9 and 15.4, of 2048
+    // 22.3 and 20.2; 80 rows of 1024 14.4 and 16.4; 2 of 512 10.3 to 14.3 (the host's time) and 10.3 to 11.1, with 12 heads,
+    // which take two passes, 12.3 and 14.4
+    const bool fill = 4 * (int64_t)rows >= 3 * sm_count(), brief = a.c.n_b <= 512 && a.G <= KV_SCORE_G;
+    if (rows <= (unsigned)sm_count() && a.c.n_b <= KV_ROW_THREADS * KV_ROW_KEYS && (fill || brief)) {
+        if (q_dtype == MILO_BF16) k_kv_select_row<__nv_bfloat16><<<rows, KV_ROW_THREADS, 0, s>>>(a);
+        else k_kv_select_row<float><<<rows, KV_ROW_THREADS, 0, s>>>(a);
+        e = cudaGetLastError();
+    } else {
+        // blocks per CTA: as many steps of its warps as leave one wave of four CTAs an SM (a CTA first codes its queries, about
+        // what two steps cost)
+        const int64_t steps = (a.c.n_b + KV_SCORE_STEP - 1) / KV_SCORE_STEP, wave = 4 * sm_count();
+        const int per = KV_SCORE_STEP * (int)std::min<int64_t>((rows * steps + wave - 1) / wave, steps);
+        const dim3 grid(rows, (unsigned)((a.c.n_b + per - 1) / per));
+        if (q_dtype == MILO_BF16) k_kv_score<__nv_bfloat16><<<grid, 32 * KV_SCORE_WARPS, 0, s>>>(a, per);
+        else k_kv_score<float><<<grid, 32 * KV_SCORE_WARPS, 0, s>>>(a, per);
+        e = cudaGetLastError();
+        if (e == cudaSuccess)
+            e = a.c.n_b <= 2048   ? kv_follow(k_kv_topn<512, 4, true>, dim3(rows), 512, a, s)
+                : a.c.n_b <= 8192 ? kv_follow(k_kv_topn<1024, 8, true>, dim3(rows), 1024, a, s)
+                                  : kv_follow(k_kv_topn<1024, 1, false>, dim3(rows), 1024, a, s);
+    }
     tpush(MILO_TK_KV_SELECT, t0, tmark(s));
     return cuda_check(e, "kv select launch");
 }

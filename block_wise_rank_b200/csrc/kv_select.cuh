@@ -9,11 +9,10 @@
 // so that equal blocks tie and every run picks the same ones.
 //
 // Measured on 32 sessions of 30000 to 131072 tokens, 4 KV heads of 7 query heads,
-// blocks of 64: 23 us for both kernels.  The scores take about 14 of them for 42 MB
-// (6.6 us at the copy rate): a CTA is a chain of latencies, its length, its queries'
-// coding and then up to seven steps of one batch of loads (two batches in flight cost
-// registers, 25 us in all; equal runs of steps by the lengths begin more rows, 24 us).  The
-// selection is a chain of short rounds, 6 to 9 us however few the rows are.
+// blocks of 64: 22.5 us for 42 MB (6.6 us at the copy rate), in one kernel or in two.
+// A CTA is a chain of latencies: its length, its queries' coding, then steps of one
+// batch of loads (two batches in flight cost registers, 25 us in all; equal runs of steps
+// by the lengths begin more rows, 24 us), and for the selection 6 to 9 us of short rounds.
 #pragma once
 #include "kv_cache.cuh"
 
@@ -58,7 +57,8 @@ __device__ __forceinline__ void kv_imma(int (&c)[4], uint32_t a0, uint32_t a1, u
 // the query heads its columns.  The sum's order is free: thread c of a row's four
 // reads 16-byte chunks c, c + 4, c + 8, c + 12 of a block's 256 bytes, which are the
 // operands of two steps each.  Bound by reading the codes once (260 B a block).
-template <typename T> __global__ void __launch_bounds__(32 * KV_SCORE_WARPS) k_kv_score(KvSelectArgs a, int per) {
+template <typename T, int WARPS> __device__ __forceinline__ void kv_score(const KvSelectArgs &a, int per) {
+    constexpr int STEP = 16 * WARPS;
     __shared__ __align__(16) uint32_t s_q[KV_SCORE_G][2 * D / 4];
     __shared__ float s_u[KV_SCORE_G];
     const int64_t row = blockIdx.x;
@@ -72,7 +72,7 @@ template <typename T> __global__ void __launch_bounds__(32 * KV_SCORE_WARPS) k_k
     const int b0 = blockIdx.y * per, b1 = min(a.c.n_b, b0 + per);
     float *out = a.scores + row * a.c.n_b;
     kv_launch_next();
-    for (int b = max(b0, cand) + tid; b < b1; b += 32 * KV_SCORE_WARPS) out[b] = -INFINITY;
+    for (int b = max(b0, cand) + tid; b < b1; b += 32 * WARPS) out[b] = -INFINITY;
     if (b0 >= cand) return;
     const int end = min(b1, cand);
     const int64_t base = ((int64_t)s * a.c.H + h) * a.c.n_b;
@@ -96,7 +96,7 @@ template <typename T> __global__ void __launch_bounds__(32 * KV_SCORE_WARPS) k_k
             __syncthreads();                        // the heads before these are used
             load(b0 + 16 * warp);
         }
-        for (int gg = warp; gg < KV_SCORE_G; gg += KV_SCORE_WARPS) {   // a head's codes; lane holds channels 4 lane ..
+        for (int gg = warp; gg < KV_SCORE_G; gg += WARPS) {   // a head's codes; lane holds channels 4 lane ..
             uint32_t neg = 0u, pos = 0u;
             float u = 0.f;
             if (gg < gn) {
@@ -131,14 +131,14 @@ template <typename T> __global__ void __launch_bounds__(32 * KV_SCORE_WARPS) k_k
 #pragma unroll
         for (int x = 0; x < 4; ++x) f[x] = *reinterpret_cast<const uint4 *>(&s_q[g][4 * c + 16 * x]);
         const float u0 = s_u[2 * c], u1 = s_u[2 * c + 1];
-        for (int b = b0 + 16 * warp; b < end; b += KV_SCORE_STEP) {
+        for (int b = b0 + 16 * warp; b < end; b += STEP) {
             int acc[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 kv_imma(acc, w[0][x].x, w[1][x].x, w[0][x].y, w[1][x].y, f[x].x, f[x].y);
                 kv_imma(acc, w[0][x].z, w[1][x].z, w[0][x].w, w[1][x].w, f[x].z, f[x].w);
             }
-            load(b + KV_SCORE_STEP);
+            load(b + STEP);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 float v = 2 * c < gn ? __fmul_rn((float)acc[2 * r], u0) : -INFINITY;
@@ -154,6 +154,9 @@ template <typename T> __global__ void __launch_bounds__(32 * KV_SCORE_WARPS) k_k
         }
     }
 }
+template <typename T> __global__ void __launch_bounds__(32 * KV_SCORE_WARPS) k_kv_score(KvSelectArgs a, int per) {
+    kv_score<T, KV_SCORE_WARPS>(a, per);
+}
 
 // larger float = larger key, 1 at least and below 2^32 - 1 (only NaN would be either)
 __device__ __forceinline__ uint32_t kv_key(float x) {
@@ -167,10 +170,9 @@ __device__ __forceinline__ uint32_t kv_key(float x) {
 // consecutive keys in registers, so that ids come out in order after one scan;
 // HELD = false reads them from the scores again in every round (more blocks than
 // THREADS * KEYS).
-template <int THREADS, int KEYS, bool HELD> __global__ void __launch_bounds__(THREADS) k_kv_topn(KvSelectArgs a) {
+template <int THREADS, int KEYS, bool HELD> __device__ __forceinline__ void kv_topn(const KvSelectArgs &a) {
     constexpr int WARPS = THREADS / 32;
     __shared__ int s_n[2][WARPS][4];
-    kv_wait_previous();
     const int64_t row = blockIdx.x;
     const int64_t lsi = row / a.c.H;
     const int i = (int)(lsi % a.n_q), s = (int)((lsi / a.n_q) % a.c.S);
@@ -299,6 +301,19 @@ template <int THREADS, int KEYS, bool HELD> __global__ void __launch_bounds__(TH
     } else {
         for (int x = 0; x < mine; ++x) put(key_of(first + x), first + x);
     }
+}
+
+template <int THREADS, int KEYS, bool HELD> __global__ void __launch_bounds__(THREADS) k_kv_topn(KvSelectArgs a) {
+    kv_wait_previous();
+    kv_topn<THREADS, KEYS, HELD>(a);
+}
+
+// Both in one CTA per row, for few blocks: the scores are the CTA's own
+constexpr int KV_ROW_THREADS = 512, KV_ROW_KEYS = 4;
+template <typename T> __global__ void __launch_bounds__(KV_ROW_THREADS) k_kv_select_row(KvSelectArgs a) {
+    kv_score<T, KV_ROW_THREADS / 32>(a, a.c.n_b);
+    __syncthreads();
+    kv_topn<KV_ROW_THREADS, KV_ROW_KEYS, true>(a);
 }
 
 }  // namespace milo

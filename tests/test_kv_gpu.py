@@ -414,6 +414,28 @@ def test_select(G, dt, bl, cap, n_q):
     ok()
 
 
+@pytest.mark.parametrize("S,H,cap,G", [(40, 4, 600, 7), (3, 2, 9000, 7), (30, 4, 9000, 8), (30, 4, 30000, 3), (4, 2, 1000, 12)])
+def test_select_by_rows_and_blocks(S, H, cap, G):
+    """Rows and blocks that one kernel takes, and that two do."""
+    c = make(1, S, H, cap, 16, "int8")
+    k = rnd(57, 1, S, H, cap, 128, dtype=BF)
+    append(c, k, k, [0] * S)
+    length = [cap - 7 * s for s in range(S)]
+    length[:3] = [0, 1, 16 * 9]
+    q = rnd(58, 1, S, H * G, 128)
+    got, _ = sections(c)
+    sel, sc = milo.milo_kv_select(c, q, i32(length), 9, 1, 2, return_scores=True)
+    assert torch.equal(sel, milo.milo_kv_select(c, q, i32(length), 9, 1, 2))
+    ok()
+    sel, sc, qn = sel.cpu().numpy(), sc.cpu().numpy(), f32np(q)
+    for s, h in np.ndindex(S, H):
+        cand = -(-length[s] // 16)
+        ref = R.scores(qn[0, s, h * G:(h + 1) * G], got["codes"][0, s, h], got["scale"][0, s, h])
+        np.testing.assert_array_equal(sc[0, s, h, :cand], ref[:cand])
+        assert np.all(np.isneginf(sc[0, s, h, cand:]))
+        np.testing.assert_array_equal(sel[0, s, h], R.top(ref, cand, 9, 1, 2))
+
+
 @pytest.mark.parametrize("n_b,n_sel,nf,nl", [(2500, 40, 2, 3), (2500, 2499, 0, 0), (9000, 100, 1, 1), (9000, 8500, 0, 0),
                                              (9000, 2, 1, 1)])
 def test_select_many_blocks(n_b, n_sel, nf, nl):
