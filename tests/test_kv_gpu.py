@@ -891,3 +891,48 @@ def test_stage_timing_counts_the_calls():
     milo.milo_timing_enable(False)
     for name in ("rope", "kv_write", "kv_read", "kv_select", "kv_attn"):
         assert t[name][1] == 1 and t[name][0] > 0
+
+
+@pytest.mark.parametrize("workload,factors", [("toy", "f32"), ("qwen3b-1layer", "bf16")])
+@pytest.mark.parametrize("dtype", KINDS)
+def test_decode_over_blocks_and_cache_shows_queries_that_are_not_finite(dtype, workload, factors):
+    """As milo_kv_attn: such a row is not finite, and its neighbours are what they were."""
+    w = synth.WORKLOADS[workload]
+    K, V = synth.workload_cache(w)
+    f = milo.milo_compress(K.cuda(), V.cuda(), w.block_len, milo.default_params(factor_dtype=factors))
+    S, Hq = 2, 4 * w.H
+    q = rnd(60, w.L, S, Hq, 128)
+    sel = i32([[0, 3], [2, 1]])
+    c = filled(w.L, S, w.H, 100, 16, dtype, [100, 100], seed=61)
+    call = lambda x, n: milo.milo_decode_attn_kv(f, x, sel, c, i32(n))  # noqa: E731
+    want = call(q, [100, 37])
+    bad = q.clone()
+    bad[0, 0, 1, 5], bad[0, 1, 3, 0] = math.nan, math.inf
+    got = call(bad, [100, 37])
+    rows = ~torch.isfinite(bad).all(-1)
+    assert int(rows.sum()) == 2 and not torch.isfinite(got[rows]).any()
+    # both factor types against their own call without the two rows; half precision's weights may move by a reference's change
+    near = 0.0 if factors == "f32" else 1e-3
+    assert float((got[~rows] - want[~rows]).abs().max()) <= near * float(want.abs().max())
+    # nothing cached: milo_decode_attn's output, whatever the queries are
+    alone = milo.milo_decode_attn(f, bad, sel)
+    assert torch.equal(call(bad, [0, 0]).view(torch.int32), alone.view(torch.int32))
+    ok()
+
+
+def test_decode_over_blocks_and_cache_shows_scores_that_overflow():
+    """Scores past fp32's end in the cache do not leave the blocks' output standing alone."""
+    w = synth.WORKLOADS["toy"]
+    K, V = synth.workload_cache(w)
+    f = milo.milo_compress(K.cuda(), V.cuda(), w.block_len, milo.default_params(factor_dtype="f32"))
+    c = make(1, 1, 1, 32, 16, "int8")
+    k = rnd(62, 1, 1, 1, 20, 128)
+    append(c, k * 1e30, k, [0])
+    q = rnd(63, 1, 1, 3, 128)
+    q[0, 0, 1] *= 1e12
+    sel = i32([[0, 3]])
+    alone = milo.milo_kv_attn(c, q, i32([20]))
+    got = milo.milo_decode_attn_kv(f, q, sel, c, i32([20]))
+    assert not torch.isfinite(alone[0, 0, 1]).any() and not torch.isfinite(got[0, 0, 1]).any()
+    assert torch.isfinite(got[0, 0, [0, 2]]).all()
+    ok()
