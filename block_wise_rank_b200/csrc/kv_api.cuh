@@ -211,13 +211,21 @@ template <typename T, int NT, bool SEL> cudaError_t kv_attn_merge(const KvAttnAr
     return kv_follow(k_kv_attn_merge<T, NT, SEL>, dim3(grid, rows), 32 * KA_MERGE_WARPS, a, s);
 }
 
-template <typename T, int DT, int NT, bool SEL> cudaError_t kv_attn_run(const KvAttnArgs &a, int grid, cudaStream_t s) {
+template <typename T, int DT, int NT, bool SEL, bool OWN>
+cudaError_t kv_attn_run_as(const KvAttnArgs &a, int grid, cudaStream_t s) {
     static bool done[64];
     const size_t smem = sizeof(KaSmem<T, DT, NT>);
-    const cudaError_t e = kv_smem(k_kv_attn<T, DT, NT, SEL>, smem, done);
+    const cudaError_t e = kv_smem(k_kv_attn<T, DT, NT, SEL, OWN>, smem, done);
     if (e != cudaSuccess) return e;
-    k_kv_attn<T, DT, NT, SEL><<<grid, 32 * KaShape<NT>::WARPS, smem, s>>>(a);
+    k_kv_attn<T, DT, NT, SEL, OWN><<<grid, 32 * KaShape<NT>::WARPS, smem, s>>>(a);
     return kv_attn_merge<T, NT, SEL>(a, grid, s);
+}
+
+template <typename T, int DT, int NT, bool SEL> cudaError_t kv_attn_run(const KvAttnArgs &a, int grid, cudaStream_t s) {
+    // rows of a line that see different tokens: the queries of a session, where they are not lines of their own
+    if constexpr (!SEL && DT != MILO_INT4)
+        if (a.n_q > 1) return kv_attn_run_as<T, DT, NT, SEL, true>(a, grid, s);
+    return kv_attn_run_as<T, DT, NT, SEL, false>(a, grid, s);
 }
 
 template <typename T, int DT> cudaError_t kv_attn_run_wide(const KvAttnArgs &a, int grid, cudaStream_t s) {

@@ -16,7 +16,10 @@
 //   value it stands for).
 // * Row scales never touch the rows: the key's multiplies the score, the
 //   value's the weight.  A weight is kept as p * v_scale / 2^E * 2^10 in fp16,
-//   with E the greatest exponent of the scales so far.
+//   with E the greatest exponent of the scales so far.  Where the queries of a line
+//   see different tokens (OWN: several queries over all tokens) each row has an E of
+//   its own, from the tokens that it sees: another query's token may be any size
+//   (1 to 4 % of such a call: 2 queries of 8 heads over 30000 tokens 61.2 -> 63.2 us).
 // * fp32 queries go in two fp16 parts (22 bits, after a power of two that puts
 //   the row's greatest value at 2^8), and so do their weights; bf16 queries fit in
 //   one part, and their weights are rounded to fp16 (2^-11, an eighth of the
@@ -39,6 +42,8 @@
 // tokens, 190 of them widening the codes).  A short line costs a CTA about 4 us beside its
 // tokens.
 #pragma once
+#include <type_traits>
+
 #include "kv_select.cuh"
 
 namespace milo {
@@ -492,7 +497,7 @@ template <typename T, int DT, int NT> struct KaSmem {
     unsigned char ring[KA_WARPS][RING > OUT ? RING : OUT];   // a warp's stages; behind its tiles its output [RPT][D + 4]
     uint32_t q[NT][8][32][2 * PARTS];                        // fragments of the queries, [tile][step][lane]
     float m[KA_WARPS][RPT], l[KA_WARPS][RPT];
-    float e[KA_WARPS + 1];                                   // 2^E of the warps' value scales, and of the join
+    float e[KA_WARPS + 1][RPT];                              // 2^E of the warps' value scales, and the join's factor
     float sc[RPT];                                           // factor on a row's scores
     int seen[RPT];
     int t0[KA_WARPS][KaTile<DT>::STAGES];                    // first token of the tile in each stage
@@ -519,13 +524,15 @@ __device__ __forceinline__ void ka_finish(const KvAttnArgs &a, int64_t row, int 
     if (lane == 0) ka_finish_sums(a, row, m, l);
 }
 
-template <typename T, int DT, int NT, bool SEL>
+template <typename T, int DT, int NT, bool SEL, bool OWN>
 __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_kv_attn(const __grid_constant__ KvAttnArgs a) {
     using Sm = KaSmem<T, DT, NT>;
     using Tl = KaTile<DT>;
     constexpr int RPT = Sm::RPT, PARTS = Sm::PARTS, KA_WARPS = Sm::KA_WARPS;
     constexpr int KA_BEGIN = KaShape<NT>::BEGIN;
     constexpr bool PAR = DT != MILO_INT4;                    // a scale per row
+    static_assert(PAR || !OWN, "only scales per row have an E");
+    constexpr int EN = OWN ? NT : 1, EX = OWN ? 2 : 1;       // its values: the lane's query rows, or one
     extern __shared__ __align__(16) unsigned char ka_raw[];
     Sm &sm = *reinterpret_cast<Sm *>(ka_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
@@ -639,7 +646,11 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
 #pragma unroll
                 for (int w = 0; w < 8; ++w) o[n][w][2 * x] = o[n][w][2 * x + 1] = 0.f;
             }
-        float e_max = 0.f, e_inv = 0.f;                      // 2^E and 2^(10 - E) of the value scales so far
+        float e_max[EN][EX], e_inv[EN][EX];                  // 2^E and 2^(10 - E) of the value scales so far
+#pragma unroll
+        for (int n = 0; n < EN; ++n)
+#pragma unroll
+            for (int x = 0; x < EX; ++x) e_max[n][x] = e_inv[n][x] = 0.f;
 
         for (int stage = 0; left > 0; --left) {
             ka_wait<AHEAD - 1>();
@@ -717,43 +728,73 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
                         }
                     }
             }
+            const bool edge = OWN && t0 + 16 > least;        // some row does not see all of the tile, nor of those behind it
             if constexpr (PAR) {
-                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs[0], vs[1])));
-                const float pw = __uint_as_float(min(max(top & 0x7f800000u, KA_E_MIN), 0x7e800000u));   // 2^E
-                if (pw > e_max) {
-                    const float f = e_max * (1.f / pw);
+                // 2^E of the greatest scale; a row's (n, x), or all rows' at once
+                auto raise_e = [&](uint32_t top, int n0, int n1, int x0, int step) {
+                    const float pw = __uint_as_float(min(max(top & 0x7f800000u, KA_E_MIN), 0x7e800000u));
+                    float &e = e_max[OWN ? n0 : 0][OWN ? x0 : 0];
+                    if (pw <= e) return;
+                    const float f = e * (1.f / pw);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int w = 0; w < 8; ++w)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) o[n][w][x] *= f;
-                    e_max = pw;
-                    e_inv = KA_UP / pw;
+                            for (int i = 0; i < 4; ++i)
+                                if (n >= n0 && n < n1 && i % step == x0) o[n][w][i] *= f;
+#pragma unroll
+                    for (int n = 0; n < EN; ++n)
+#pragma unroll
+                        for (int x = 0; x < EX; ++x)
+                            if (n >= n0 && n < n1 && x % step == x0) {
+                                e_max[n][x] = pw;
+                                e_inv[n][x] = KA_UP / pw;
+                            }
+                };
+                if (!edge) {                                 // every row has seen the same so far
+                    raise_e(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(vs[0], vs[1]))), 0, NT, 0, 1);
+                    vs[0] *= e_inv[0][0];
+                    vs[1] *= e_inv[0][0];
+                } else {
+#pragma unroll
+                    for (int n = 0; n < EN; ++n)
+#pragma unroll
+                        for (int x = 0; x < EX; ++x) {
+                            const float v = fmaxf(y[n][x] == -INFINITY ? 0.f : vs[0], y[n][2 + x] == -INFINITY ? 0.f : vs[1]);
+                            uint32_t u = __float_as_uint(v);
+#pragma unroll
+                            for (int w = 4; w < 32; w <<= 1) u = max(u, __shfl_xor_sync(0xffffffffu, u, w));
+                            raise_e(u, n, n + 1, x, 2);
+                        }
                 }
-                vs[0] *= e_inv;
-                vs[1] *= e_inv;
             }
             // weights, as fragments of the value product
             uint32_t b[NT][2][PARTS];
+            auto weights = [&](auto at_edge) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float p[4];
+                for (int n = 0; n < NT; ++n) {
+                    float p[4];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    p[x] = ka_exp2(y[n][x]);
-                    sum[n][x % 2] += p[x];
-                    p[x] *= PAR ? vs[x / 2] : KA_UP;
+                    for (int x = 0; x < 4; ++x) {
+                        p[x] = ka_exp2(y[n][x]);
+                        sum[n][x % 2] += p[x];
+                        p[x] *= PAR ? vs[x / 2] : KA_UP;
+                        // last: 0 for a token not seen, whatever its scale is
+                        if constexpr (decltype(at_edge)::value) p[x] *= e_inv[n][x % 2];
+                    }
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const __half2 hi = __floats2half2_rn(p[2 * r], p[2 * r + 1]);
+                        b[n][r][0] = ka_transpose(ka_u(hi));
+                        if constexpr (PARTS == 2)
+                            b[n][r][1] = ka_transpose(ka_u(__floats2half2_rn(p[2 * r] - __low2float(hi),
+                                                                             p[2 * r + 1] - __high2float(hi))));
+                    }
                 }
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const __half2 hi = __floats2half2_rn(p[2 * r], p[2 * r + 1]);
-                    b[n][r][0] = ka_transpose(ka_u(hi));
-                    if constexpr (PARTS == 2)
-                        b[n][r][1] = ka_transpose(ka_u(__floats2half2_rn(p[2 * r] - __low2float(hi),
-                                                                         p[2 * r + 1] - __high2float(hi))));
-                }
-            }
+            };
+            if (OWN && edge) weights(std::integral_constant<bool, OWN>());
+            else weights(std::false_type());
             KaValues<DT> vals;
             ka_read_v<DT>(st, g, c, vals);
 #pragma unroll
@@ -783,13 +824,13 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
                 if (g == 0) {
                     sm.m[warp][r] = -off[n][x];
                     sm.l[warp][r] = sum[n][x];
+                    sm.e[warp][r] = PAR ? e_max[OWN ? n : 0][OWN ? x : 0] : 1.f;
                 }
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
                     *reinterpret_cast<float4 *>(my_o + r * (D + 4) + 16 * g + 4 * w) =
                         make_float4(o[n][2 * w][x], o[n][2 * w][2 + x], o[n][2 * w + 1][x], o[n][2 * w + 1][2 + x]);
             }
-        if (lane == 0) sm.e[warp] = PAR ? e_max : 1.f;
         __syncthreads();
         const bool whole = s0 == 0 && s1 == run.per;
         const int64_t part = 2 * (int64_t)blockIdx.x + (s0 == 0 ? 1 : 0);
@@ -797,7 +838,7 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
             float e_top = 0.f, m = -INFINITY, den = 0.f;
 #pragma unroll
             for (int w = 0; w < KA_WARPS; ++w) {
-                e_top = fmaxf(e_top, sm.e[w]);
+                e_top = fmaxf(e_top, sm.e[w][tid]);
                 m = fmaxf(m, sm.m[w][tid]);
             }
             float f[KA_WARPS];
@@ -808,10 +849,10 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
             }
             const float inv = den != 0.f ? 1.f / den : 0.f, down = e_top > 0.f ? 1.f / e_top : 0.f;
 #pragma unroll
-            for (int w = 0; w < KA_WARPS; ++w) sm.m[w][tid] = f[w] * inv * (sm.e[w] * down);
+            for (int w = 0; w < KA_WARPS; ++w) sm.m[w][tid] = f[w] * inv * (sm.e[w][tid] * down);
             sm.l[0][tid] = den;
             sm.sc[tid] = m;
-            if (tid == 0) sm.e[KA_WARPS] = e_top * ((DT == MILO_FP8 ? KA_FP8_UP : 1.f) / KA_UP);
+            sm.e[KA_WARPS][tid] = e_top * ((DT == MILO_FP8 ? KA_FP8_UP : 1.f) / KA_UP);
         }
         __syncthreads();
         for (int r = warp; r < cl.rows; r += KA_WARPS) {     // a row per warp, four channels a lane
@@ -825,7 +866,7 @@ __global__ void __launch_bounds__(32 * KaShape<NT>::WARPS, KaShape<NT>::CTAS) k_
                 y.z = fmaf(f, x.z, y.z);
                 y.w = fmaf(f, x.w, y.w);
             }
-            const float up = sm.e[KA_WARPS];
+            const float up = sm.e[KA_WARPS][r];
             y = make_float4(y.x * up, y.y * up, y.z * up, y.w * up);
             if (whole) ka_finish<T>(a, cl.row(a, l, h, r), lane, y, sm.sc[r], sm.l[0][r]);
             else {

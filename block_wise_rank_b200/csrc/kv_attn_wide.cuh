@@ -10,8 +10,8 @@
 //   - S = Q K^T, M = N = 128, fp32 in tensor memory, Q in one (bf16) or two
 //     (fp32) fp16 parts from shared memory;
 //   - each thread takes a quarter of one query row's scores: scales, mask,
-//     running reference and sum as in k_kv_attn, the weights packed to fp16
-//     parts back into tensor memory;
+//     running reference, sum and value exponent of the row as in k_kv_attn, the
+//     weights packed to fp16 parts back into tensor memory;
 //   - O += P V with P from tensor memory, while the next tile's S is formed.
 // Measured on 17 fp32 queries of 7 heads over 20 to 8190 e4m3 tokens of 4 sessions, 4
 // heads, 2 layers: 52 us (k_kv_attn in tiles of 16 rows: 102 us; the bytes alone would take 6).
@@ -29,6 +29,7 @@ namespace milo {
 constexpr int KW_ROWS = 128, KW_TOK = 128, KW_THREADS = 512;
 static_assert(KW_TOK == D, "a thread's columns of the scores are also its columns of the output");
 constexpr int KW_SPLIT = KW_THREADS / KW_ROWS, KW_COLS = KW_TOK / KW_SPLIT;   // threads of a query row, tokens of each
+static_assert(KW_SPLIT == 4, "a row's threads exchange four values");
 constexpr int KW_WARPS = KW_THREADS / 32, KW_TAKE = KW_TOK * 8 / KW_THREADS;  // 16-channel pieces of a tile that a thread widens
 constexpr uint32_t KW_TMEM = 512, KW_S = 0, KW_O = 128, KW_P = 256;   // columns: scores, output, weights (2 parts of 64)
 constexpr int KW_TILE = KW_TOK * D * 2;                               // bytes of a widened tile
@@ -38,9 +39,11 @@ template <typename T> struct KwSmem {
     unsigned char q[PARTS][KW_TILE], k[2][KW_TILE], v[2][KW_TILE];
     float ks[2][KW_TOK], vs[2][KW_TOK];       // scales of a tile's rows
     float top[2][4];                          // greatest value scale of 32 rows each
-    float x[KW_SPLIT][KW_ROWS];               // exchange between a row's threads
+    float x[KW_SPLIT][KW_ROWS];               // exchange between a row's threads: scores, sums
+    float y[KW_SPLIT][KW_ROWS];               // value scales of the tokens that the row sees
     float sc[KW_ROWS];
     int seen[KW_ROWS];
+    int least;                                // tokens that every row sees
     KaScan scan;
     uint64_t bar_s, bar_o;                    // S formed; P V added
     uint32_t tmem;
@@ -276,6 +279,7 @@ template <typename T, int DT> __global__ void __launch_bounds__(KW_THREADS, 1) k
             if (x == 0) {
                 sm.sc[r] = a.scale * UP * down;
                 sm.seen[r] = live ? cl.seen(a, r) : end;
+                if (r == 0) sm.least = sm.seen[0];
             }
         }
         if (n > 0) {
@@ -338,6 +342,12 @@ template <typename T, int DT> __global__ void __launch_bounds__(KW_THREADS, 1) k
 #pragma unroll
                 for (int c = 0; c < KW_COLS; ++c) top = fmaxf(top, z[c]);
                 sm.x[warp / 4][row] = top;
+                const bool edge = PAR && (first + i + 1) * KW_TOK > sm.least;   // some row does not see all of the tile
+                if (edge) {
+                    float w = 0.f;
+                    for (int c = 0; c < min(KW_COLS, seen - t0); ++c) w = fmaxf(w, sm.vs[buf][col + c]);
+                    sm.y[warp / 4][row] = w;
+                }
                 kw_rows_sync(warp);
 #pragma unroll
                 for (int y = 0; y < KW_SPLIT; ++y) top = fmaxf(top, sm.x[y][row]);
@@ -347,7 +357,8 @@ template <typename T, int DT> __global__ void __launch_bounds__(KW_THREADS, 1) k
                     rescale = true;
                 }
                 if (PAR) {
-                    const float4 t4 = *reinterpret_cast<const float4 *>(sm.top[buf]);
+                    float4 t4 = *reinterpret_cast<const float4 *>(sm.top[buf]);
+                    if (edge) t4 = make_float4(sm.y[0][row], sm.y[1][row], sm.y[2][row], sm.y[3][row]);
                     const uint32_t bits = __float_as_uint(fmaxf(fmaxf(t4.x, t4.y), fmaxf(t4.z, t4.w))) & 0x7f800000u;
                     const float pw = __uint_as_float(min(max(bits, KA_E_MIN), 0x7e800000u));   // 2^E
                     sum *= fac;
@@ -394,7 +405,8 @@ template <typename T, int DT> __global__ void __launch_bounds__(KW_THREADS, 1) k
                         for (int e = 0; e < 4; ++e) {
                             p[e] = ka_exp2(z[16 * b + c + e] + off);
                             sum += p[e];
-                            p[e] *= PAR ? w[e] * e_inv : KA_UP;
+                            p[e] *= PAR ? w[e] : KA_UP;
+                            if (PAR) p[e] *= e_inv;        // last: 0 for a token not seen, whatever its scale is
                         }
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {

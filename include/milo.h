@@ -545,6 +545,10 @@ size_t milo_kv_attn_workspace_size(const milo_kv_shape *shape, int32_t n_q, int3
  *   q, out:   device, q_dtype (MILO_F32 or MILO_BF16), [L][S][n_q][Hq][d], 16-byte
  *             aligned; q already rotated.  Products and sums are held to fp32 for
  *             MILO_F32; MILO_BF16 rounds the softmax weights to fp16.
+ *             In an INT8 or FP8 cache a token's part is moreover held to 2^-34 of
+ *             the greatest value that its query sees: values far below that lose
+ *             bits.  Tokens that a query does not see change nothing, whatever
+ *             their size.
  *   len:      as milo_kv_select
  *   selected: device, int32 [L][S][n_q][H][n_sel] block ids (as milo_kv_select
  *             writes them; any order), -1 = none, or NULL for all tokens (n_sel =

@@ -936,3 +936,21 @@ def test_decode_over_blocks_and_cache_shows_scores_that_overflow():
     assert not torch.isfinite(alone[0, 0, 1]).any() and not torch.isfinite(got[0, 0, 1]).any()
     assert torch.isfinite(got[0, 0, [0, 2]]).all()
     ok()
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("n_q,G,H", [(2, 3, 2), (16, 1, 1), (3, 7, 1), (100, 2, 1)])
+@pytest.mark.parametrize("cap", [300, 6000])
+def test_attn_tokens_that_a_query_does_not_see_cost_it_nothing(dtype, dt, n_q, G, H, cap):
+    """The last tokens' values are larger and larger: a query sees its own and those before it, and is as exact as they
+    alone make it (the bound counts the values that it sees)."""
+    L, S, n = 1, 3, 290
+    c = make(L, S, H, cap, 16, dtype)
+    k, v = rnd(64, L, S, H, n, 128), rnd(65, L, S, H, n, 128)
+    top = 12.0 if dtype == "int4" else 110.0                     # 2^top at the last token
+    grow = torch.zeros(n)
+    grow[n - n_q:] = torch.linspace(top / n_q, top, n_q)
+    append(c, k, v * torch.exp2(grow.round()).cuda()[:, None], [0] * S)
+    ok()
+    check_attn(c, rnd(66, L, S, n_q, G * H, 128, dtype=dt), [n, n - n_q + 1, n - 17])
