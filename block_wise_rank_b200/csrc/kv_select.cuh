@@ -1,9 +1,11 @@
 // kv_select.cuh -- retrieval by query: the blocks of the recent-token cache
-// whose keys can score highest.
+// whose keys are estimated to score highest.
 //
-// For a query c (INT8 codes) and a block whose keys lie channelwise in
-// [lo, hi], sum_j max(c_j lo_j, c_j hi_j) bounds c . k from above for every
-// key of the block.  With both sides in INT8 the sum is
+// For a query q and a block whose keys lie channelwise in [lo, hi],
+// sum_j max(q_j lo_j, q_j hi_j) bounds q . k from above for every key of the
+// block.  Both sides are rounded to the nearest INT8 code, which makes the sum an
+// estimate: it may miss the bound by half a step of the query's codes and of the
+// bounds' (milo.h has the slack).  In codes it is
 //   sum_j min(c_j, 0) lo_j + max(c_j, 0) hi_j,
 // one dot product of 256 8-bit values, exact in integers whatever the order,
 // so that equal blocks tie and every run picks the same ones.

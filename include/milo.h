@@ -508,16 +508,21 @@ milo_status milo_kv_read(const milo_kv_shape *shape, const void *cache, size_t c
 size_t milo_kv_select_workspace_size(const milo_kv_shape *shape, int32_t n_q);
 
 /*
- * Retrieval by query: the n_sel blocks of the cache with the greatest upper
- * bound of q . k, per layer, session, query and KV head.  The query-vector
+ * Retrieval by query: the n_sel blocks of the cache whose keys are estimated to
+ * reach the greatest q . k, per layer, session, query and KV head.  The query-vector
  * counterpart of milo_bm25_select, for the cache of recent tokens.  Query i of
  * session s sees the tokens t <= len[s] - n_q + i (the last n_q tokens held are
  * the queries' own); blocks that begin behind that are not candidates.  With
  * the query's INT8 codes c_j = rint(q_j / u), u = max|q| / 127, and the
- * block's bound codes lo_j, hi_j with scale s, a query head's bound is
+ * block's bound codes lo_j, hi_j with scale s, a query head's estimate is
  *   (sum_j max(c_j lo_j, c_j hi_j)) * u        (the sum exact in integers)
  * and the block's score the greatest over the G = Hq / H query heads of the KV
- * head, times s.
+ * head, times s.  Without the codes' roundings this would be an upper bound of
+ * q . k.  With them a score is at least q . k of every key of the block less
+ *   u / 2 sum_j |k_j|  +  s / 2 sum_j |u c_j|
+ * (half a step of the query's codes and of the bounds'; the score's own fp32
+ * roundings aside): s follows the block's loudest channel, so one channel far
+ * above the others makes the estimate coarse in all of them.
  *   q:        device, q_dtype (MILO_F32 or MILO_BF16), [L][S][n_q][Hq][d], 16-byte aligned
  *   len:      device, int32 [S], tokens held; outside [0, cap] sets
  *             MILO_ERR_BOUNDS and counts as 0

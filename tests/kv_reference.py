@@ -153,3 +153,14 @@ def attn(q, k, v, scale, f16_weights=False, out_eps=0.0):
     err = err + out_eps * np.abs(o) + 1e-30
     lse = (m + np.log(l))[:, 0]
     return o, lse, err, (w * (dz + 2.0 ** -21 + steps)).sum(-1) + 2.0 ** -23 * (1 + np.abs(lse))
+
+
+def score_floor(q, k, s):
+    """The least score [G], before its own fp32 roundings, of query heads q [G][128] for a block of keys k [T][128]
+    whose bound codes have the scale s.  With u = max|q| / 127 a code of q is at most u / 2 off and a code of a bound
+    s / 2, so the score is at least max_t (q . k_t - u / 2 sum_j |k_tj|) - s / 2 sum_j |q'_j|, q' = u c the coded q."""
+    q, k = q.astype(np.float64), k.astype(np.float64)
+    u = np.abs(q).max(-1, keepdims=True) / 127
+    coded = u * np.abs(np.rint(q / np.where(u > 0, u, 1)))
+    off = 0.5 + 2.0 ** -15           # half a step; a code of at most 127 is decided in fp32
+    return (q @ k.T - off * u * np.abs(k).sum(-1)).max(-1) - off * float(s) * coded.sum(-1)

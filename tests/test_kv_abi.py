@@ -242,3 +242,25 @@ def test_reference_attention_bound_covers_fp32():
     t = torch.from_numpy(q) @ torch.from_numpy(k).T * np.float32(128 ** -0.5)
     assert np.all(np.abs((torch.softmax(t, -1) @ torch.from_numpy(v)).numpy() - o) <= err) and err.max() < 1e-3
     assert np.all(np.abs(torch.logsumexp(t, -1).numpy() - lse) <= le)
+
+
+def test_reference_score_is_an_estimate_within_its_slack():
+    """The coded score may lie below the greatest q . k of a block, by the codes' half steps at most."""
+    below = 0
+    for seed in range(60):
+        g = np.random.default_rng(seed)
+        k = (g.standard_normal((64, 128)) + 3 * g.standard_normal(128)).astype(np.float32)
+        if seed % 3 == 1:
+            k /= 16
+            k[:, 5] = 200.0                           # one loud channel, which q does not ask for
+        if seed % 3 == 2:
+            k[:] = k[0]                                          # equal keys: no room between the bounds
+        q = g.standard_normal((3, 128)).astype(np.float32)
+        if seed % 3 == 1:
+            q[:, 5] = 0.0
+        lo, hi = R.outward(k.min(0), False), R.outward(k.max(0), True)
+        c, s = R.bound_codes(lo[None], hi[None])
+        got = float(R.scores(q, c, s)[0])
+        assert got >= R.score_floor(q, k, s[0]).max() - abs(got) * 2.0 ** -22
+        below += got < float((q @ k.T).max())
+    assert below > 0                                             # so it is no upper bound

@@ -954,3 +954,25 @@ def test_attn_tokens_that_a_query_does_not_see_cost_it_nothing(dtype, dt, n_q, G
     append(c, k, v * torch.exp2(grow.round()).cuda()[:, None], [0] * S)
     ok()
     check_attn(c, rnd(66, L, S, n_q, G * H, 128, dtype=dt), [n, n - n_q + 1, n - 17])
+
+
+@pytest.mark.parametrize("loud", [1.0, 50.0, 200.0])
+def test_select_scores_stay_within_their_slack(loud):
+    """milo_kv_select's scores are estimates: at least q . k of every key of the block less the codes' half steps."""
+    S, cap, bl = 4, 640, 64
+    c = make(1, S, 1, cap, bl, "int8")
+    k = rnd(67, 1, S, 1, cap, 128) + 3 * rnd(68, 1, S, 1, 1, 128)
+    k[..., 7] *= loud
+    k[:, 1] = k[:, 1, :, :1]                                      # blocks of equal keys: no room between the bounds
+    append(c, k, k, [0] * S)
+    q = rnd(69, 1, S, 3, 128)
+    q[:, 2, :, 7] = 0.0                                           # the loud channel is not asked for
+    _, sc = milo.milo_kv_select(c, q, i32([cap] * S), 2, return_scores=True)
+    ok()
+    sc, qn, kn = np64(sc), f32np(q), f32np(k)
+    scale = sections(c)[0]["scale"]
+    for s in range(S):
+        got = sc[0, s, 0]
+        for b in range(c.n_b):
+            best = R.score_floor(qn[0, s], kn[0, s, 0, b * bl:(b + 1) * bl], scale[0, s, 0, b])
+            assert got[b] >= best.max() - abs(got[b]) * 2.0 ** -22
