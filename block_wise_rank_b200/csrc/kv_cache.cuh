@@ -242,12 +242,13 @@ template <> struct KvBounds<__nv_bfloat16> {   // two channels an instruction
             hi[i] = __hmax2(hi[i], v[i]);
         }
     }
-    __device__ __forceinline__ void add(const float (&x)[16]) {   // x are bf16 values (or +-65440, which rounds outward)
+    __device__ __forceinline__ void add(const float (&x)[16]) {   // x are bf16 values, or +-65440: rounded outward
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            lo[i] = __hmin2(lo[i], v);
-            hi[i] = __hmax2(hi[i], v);
+            const __nv_bfloat162 d = __halves2bfloat162(__float2bfloat16_rd(x[2 * i]), __float2bfloat16_rd(x[2 * i + 1]));
+            const __nv_bfloat162 u = __halves2bfloat162(__float2bfloat16_ru(x[2 * i]), __float2bfloat16_ru(x[2 * i + 1]));
+            lo[i] = __hmin2(lo[i], d);
+            hi[i] = __hmax2(hi[i], u);
         }
     }
     __device__ __forceinline__ void get(float (&l)[16], float (&h)[16]) const {

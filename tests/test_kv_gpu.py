@@ -976,3 +976,42 @@ def test_select_scores_stay_within_their_slack(loud):
         for b in range(c.n_b):
             best = R.score_floor(qn[0, s], kn[0, s, 0, b * bl:(b + 1) * bl], scale[0, s, 0, b])
             assert got[b] >= best.max() - abs(got[b]) * 2.0 ** -22
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("n", [3, 40])
+def test_int4_bounds_of_saturated_keys_are_outward(dt, n):
+    """Keys past the INT4 limit of one sign: the bounds hold the stored +-65440 between them, in both types alike."""
+    c = make(1, 1, 1, 64, 16, "int4")
+    x = rnd(70, 1, 1, 1, n, 128, scale=10.0).to(dt)
+    x[..., 0::4], x[..., 1::4] = 70656.0, -70656.0               # both types hold them
+    x[..., 1, 0], x[..., 2, 1] = 65536.0, -65536.0
+    append(c, x, x, [0])
+    ok(milo.MILO_ERR_NONFINITE)
+    z = f32np(x).clip(-65440, 65440)
+    got, _ = sections(c)
+    q, p = R.quantise(z, "int4")
+    for name in ("k", "v"):
+        np.testing.assert_array_equal(got[name][:, :, :, :n], q)
+        np.testing.assert_array_equal(got[name + "p"][:, :, :, :n], p)
+    for b in range(-(-n // 16)):
+        t = z[0, 0, 0, 16 * b:16 * (b + 1)]
+        lo, hi = R.outward(t.min(0), False), R.outward(t.max(0), True)
+        assert lo[0] == 65280.0 and hi[0] == 65536.0 and lo[1] == -65536.0 and hi[1] == -65280.0
+        np.testing.assert_array_equal(got["bounds"][0, 0, 0, b], np.stack([lo, hi]))
+        codes, scale = R.bound_codes(lo, hi)
+        np.testing.assert_array_equal(got["codes"][0, 0, 0, b], codes)
+        assert got["scale"][0, 0, 0, b] == scale
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_int4_values_past_the_limit_are_stored_as_the_limit(dt):
+    c = make(1, 1, 1, 16, 16, "int4")
+    x = rnd(71, 1, 1, 1, 8, 128, dtype=dt)
+    x[..., 0, 0], x[..., 0, 1], x[..., 1, 0], x[..., 2, 40] = 1e38, -1e38, 65504.0, 65441.0   # bf16: 65536
+    append(c, x, x, [0])
+    ok(milo.MILO_ERR_NONFINITE)
+    q, p = R.quantise(f32np(x).clip(-65440, 65440), "int4")
+    got, _ = sections(c)
+    np.testing.assert_array_equal(got["k"][:, :, :, :8], q)
+    np.testing.assert_array_equal(got["kp"][:, :, :, :8], p)
