@@ -62,8 +62,9 @@ void rope_freqs(const milo_rope_params *p, int rd, double *w, double *m) {
         default: w[i] = t;
         }
     }
-    *m = p->attn_factor > 0.0 ? p->attn_factor
-                              : (p->scaling == MILO_ROPE_YARN ? 0.1 * std::log(p->factor) + 1.0 : 1.0);
+    // YaRN (Peng et al., 2023): 0.1 ln(factor) + 1 for a longer context, 1 for one that is not
+    const double own = p->scaling == MILO_ROPE_YARN && p->factor > 1.0 ? 0.1 * std::log(p->factor) + 1.0 : 1.0;
+    *m = p->attn_factor > 0.0 ? p->attn_factor : own;
 }
 
 // [lo, hi) bytes that n_tokens x n_heads rows of d elements cover

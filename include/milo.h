@@ -389,7 +389,7 @@ typedef struct {
     double low_freq;       /* BANDS: low_freq < high_freq (1 and 4 are usual)          */
     double high_freq;
     double attn_factor;    /* the turned channels are multiplied by this; 0 = 1, and
-                              for YARN 0 = 0.1 ln(factor) + 1                          */
+                              for YARN with factor > 1 0 = 0.1 ln(factor) + 1          */
 } milo_rope_params;
 
 /* Fill params: the given d and base, everything turned in half layout, no

@@ -264,3 +264,12 @@ def test_reference_score_is_an_estimate_within_its_slack():
         assert got >= R.score_floor(q, k, s[0]).max() - abs(got) * 2.0 ** -22
         below += got < float((q @ k.T).max())
     assert below > 0                                             # so it is no upper bound
+
+
+def test_rope_yarn_factor_below_one(L):
+    """The attention factor grows with the logarithm of a longer context; a shorter one leaves it at 1."""
+    for factor, want in ((4.0, 0.1 * math.log(4.0) + 1), (1.0, 1.0), (0.5, 1.0), (1e-5, 1.0)):
+        p = milo.rope_params(64, 1e4, scaling="yarn", factor=factor, orig_ctx=4096)
+        assert milo.milo_rope_freqs(p)[1] == pytest.approx(want, rel=1e-15)
+        p.attn_factor = 0.25
+        assert milo.milo_rope_freqs(p)[1] == 0.25
