@@ -4,6 +4,11 @@ Argument marshalling only: every step of the path runs in libmilo's CUDA
 kernels.  Tensors are passed as raw device (or host) pointers; PyTorch is
 used for device memory and streams.  There is no fallback: if libmilo.so is
 missing or fails to load, every call raises.
+
+A call with `stream` runs there, and what it makes itself (outputs, workspaces)
+is that stream's memory, as if it were called under torch.cuda.stream(stream): its
+inputs have to be ready on that stream, and another stream that reads its outputs
+waits for it first.
 """
 from __future__ import annotations
 
@@ -191,6 +196,20 @@ def _stream(stream=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _made(stream, make, *args, **kw):
+    """make(*args, **kw) in the memory of the stream that a call runs on: taken from the current stream's,
+    `stream` would use it beside earlier work that may still be under way there.  The allocator is told of the
+    current stream too, whose program goes on with the tensor."""
+    if stream is None:
+        return make(*args, **kw)
+    now = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    if t.is_cuda:
+        t.record_stream(now)
+    return t
+
+
 def _dtype_code(t: torch.dtype) -> int:
     if t == torch.float32:
         return MILO_F32
@@ -290,9 +309,9 @@ def milo_compress(K: torch.Tensor, V: torch.Tensor, block_len: int, params=None,
     if ws_n == 0 or ar_n == 0:
         raise MiloError(MILO_ERR_INVALID_ARG, "milo_compress sizes")
     if workspace is None:
-        workspace = _bytes(ws_n, K.device)
+        workspace = _made(stream, _bytes, ws_n, K.device)
     if arena is None:
-        arena = _bytes(ar_n, K.device)
+        arena = _made(stream, _bytes, ar_n, K.device)
     h = ctypes.c_void_p()
     s = lib().milo_compress(ctypes.byref(shape), _ptr(K), _ptr(V), ctypes.byref(params), _ptr(workspace),
                             workspace.numel() * workspace.element_size(), _ptr(arena),
@@ -311,9 +330,9 @@ def milo_allocate(sigma: torch.Tensor, eps: torch.Tensor, n_groups: int, n_b: in
     assert sigma.dtype == torch.float32 and eps.dtype == torch.float64 and sigma.is_contiguous()
     d = sigma.shape[-1]
     if ranks_out is None:
-        ranks_out = torch.empty(n_groups * n_b, dtype=torch.int32, device=sigma.device)
+        ranks_out = _made(stream, torch.empty, n_groups * n_b, dtype=torch.int32, device=sigma.device)
     if workspace is None:
-        workspace = _bytes(milo_allocate_workspace_size(n_groups, n_b, d), sigma.device)
+        workspace = _made(stream, _bytes, milo_allocate_workspace_size(n_groups, n_b, d), sigma.device)
     s = lib().milo_allocate(_ptr(sigma), _ptr(eps), n_groups, n_b, d, T, block_len, int(R), r_min, r_max,
                             _ptr(ranks_out), _ptr(workspace), workspace.numel(), _stream(stream))
     _check(s, "milo_allocate")
@@ -327,7 +346,7 @@ def milo_allocate_noalloc(sigma: torch.Tensor, eps: torch.Tensor, n_groups: int,
     assert sigma.dtype == torch.float32 and eps.dtype == torch.float64 and sigma.is_contiguous()
     d = sigma.shape[-1]
     if ranks_out is None:
-        ranks_out = torch.empty(n_groups * n_b, dtype=torch.int32, device=sigma.device)
+        ranks_out = _made(stream, torch.empty, n_groups * n_b, dtype=torch.int32, device=sigma.device)
     s = lib().milo_allocate_noalloc(_ptr(sigma), _ptr(eps), n_groups, n_b, d, T, block_len, int(R), r_min, r_max,
                                     _ptr(ranks_out), _stream(stream))
     _check(s, "milo_allocate_noalloc")
@@ -348,9 +367,9 @@ def milo_decode_attn(f: Factors, q: torch.Tensor, selected: torch.Tensor, positi
     if positions is not None:
         assert positions.dtype == torch.int32 and positions.shape == selected.shape and positions.is_contiguous()
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     if workspace is None:
-        workspace = _bytes(milo_decode_workspace_size(f, S, Hq, n_sel), q.device)
+        workspace = _made(stream, _bytes, milo_decode_workspace_size(f, S, Hq, n_sel), q.device)
     s = lib().milo_decode_attn(f.handle, _ptr(q), S, Hq, _ptr(selected), _ptr(positions), n_sel, float(rope_base),
                                _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream))
     _check(s, "milo_decode_attn")
@@ -379,9 +398,9 @@ def milo_decode_attn_tail(f: Factors, q: torch.Tensor, selected: torch.Tensor, k
     assert k_tail.is_contiguous() and v_tail.is_contiguous()
     assert tail_len.dtype == torch.int32 and tail_len.shape == (S,) and tail_len.is_contiguous()
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     if workspace is None:
-        workspace = _bytes(milo_decode_tail_workspace_size(f, S, Hq, n_sel), q.device)
+        workspace = _made(stream, _bytes, milo_decode_tail_workspace_size(f, S, Hq, n_sel), q.device)
     dt = MILO_BF16 if k_tail.dtype == torch.bfloat16 else MILO_F32
     s = lib().milo_decode_attn_tail(f.handle, _ptr(q), S, Hq, _ptr(selected), _ptr(positions), n_sel,
                                     float(rope_base), _ptr(k_tail), _ptr(v_tail), dt, k_tail.shape[3],
@@ -414,9 +433,9 @@ def milo_decode_attn_offload(f: Factors, q: torch.Tensor, selected: torch.Tensor
     if positions is not None:
         assert positions.dtype == torch.int32 and positions.shape == selected.shape and positions.is_contiguous()
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     if workspace is None:
-        workspace = _bytes(milo_decode_offload_workspace_size(f, S, Hq, n_sel), q.device)
+        workspace = _made(stream, _bytes, milo_decode_offload_workspace_size(f, S, Hq, n_sel), q.device)
     s = lib().milo_decode_attn_offload(f.handle, _ptr(q), S, Hq, _ptr(selected), _ptr(positions), n_sel,
                                        float(rope_base), _ptr(out), _ptr(workspace), workspace.numel(),
                                        _stream(stream))
@@ -429,13 +448,13 @@ def milo_bm25_select(tables, vocab: int, n_sel: int, k1: float = 1.2, beta: floa
     """BM25 block retrieval on the GPU.  tables = (blk_ptr, blk_term, blk_tf,
     blk_len, q_ptr, q_term, q_tf), int32 (any device).  Returns (selected
     int32 [S][n_sel], scores fp64 [S][n_b]) on `device`."""
-    t = [x.to(device=device, dtype=torch.int32).contiguous() for x in tables]
+    t = [_made(stream, lambda y: y.to(device=device, dtype=torch.int32).contiguous(), x) for x in tables]
     blk_ptr, blk_term, blk_tf, blk_len, q_ptr, q_term, q_tf = t
     n_b, S = blk_len.numel(), q_ptr.numel() - 1
-    selected = torch.empty(S, n_sel, dtype=torch.int32, device=device)
-    scores = torch.empty(S, n_b, dtype=torch.float64, device=device)
+    selected = _made(stream, torch.empty, S, n_sel, dtype=torch.int32, device=device)
+    scores = _made(stream, torch.empty, S, n_b, dtype=torch.float64, device=device)
     if workspace is None:
-        workspace = _bytes(lib().milo_bm25_workspace_size(n_b, vocab, S), device)
+        workspace = _made(stream, _bytes, lib().milo_bm25_workspace_size(n_b, vocab, S), device)
     s = lib().milo_bm25_select(_ptr(blk_ptr), _ptr(blk_term), _ptr(blk_tf), _ptr(blk_len), n_b, blk_term.numel(),
                                vocab, _ptr(q_ptr), _ptr(q_term), _ptr(q_tf), S, q_term.numel(), float(k1),
                                float(beta), n_sel, _ptr(selected), _ptr(scores), _ptr(workspace), workspace.numel(),
@@ -457,9 +476,9 @@ def milo_decode_attn_offload_tail(f: Factors, q: torch.Tensor, selected: torch.T
     assert k_tail.shape == v_tail.shape and k_tail.is_contiguous() and v_tail.is_contiguous()
     assert tail_len.dtype == torch.int32 and tail_len.shape == (S,)
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     if workspace is None:
-        workspace = _bytes(milo_decode_offload_workspace_size(f, S, Hq, n_sel), q.device)
+        workspace = _made(stream, _bytes, milo_decode_offload_workspace_size(f, S, Hq, n_sel), q.device)
     dt = MILO_BF16 if k_tail.dtype == torch.bfloat16 else MILO_F32
     s = lib().milo_decode_attn_offload_tail(f.handle, _ptr(q), S, Hq, _ptr(selected), _ptr(positions), n_sel,
                                             float(rope_base), _ptr(k_tail), _ptr(v_tail), dt, k_tail.shape[3],
@@ -501,7 +520,7 @@ def _on(t: torch.Tensor, stream) -> int:
 
 
 def _used_on(stream, *tensors):
-    """Tells the allocator that tensors made here are used on `stream`."""
+    """Tells the allocator that a call's outputs and workspace, the caller's own too, are used on `stream`."""
     if stream is not None:
         for t in tensors:
             if t is not None:
@@ -530,7 +549,7 @@ def milo_rope(x: torch.Tensor, positions: torch.Tensor, params: milo_rope_params
         raise ValueError(f"x: [n_tokens][n_heads][{params.d}] with contiguous rows expected, got {tuple(x.shape)}")
     s = _on(x, stream)
     if out is None:
-        out = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
+        out = _made(stream, torch.empty_like, x, dtype=out_dtype, memory_format=torch.contiguous_format)
     elif out.shape != x.shape or (out.numel() and out.stride(2) != 1):
         raise ValueError(f"out: {tuple(x.shape)} with contiguous rows expected, got {tuple(out.shape)}")
     n_pos = positions.numel()
@@ -631,9 +650,9 @@ def milo_kv_read(cache: KvCache, start: torch.Tensor, n: int, count=None, k_out=
     c = cache.shape
     shape = (c.L, c.S, c.H, n, c.d)
     if k_out is None:
-        k_out = cache.buf.new_empty(shape, dtype=out_dtype)
+        k_out = _made(stream, cache.buf.new_empty, shape, dtype=out_dtype)
     if v_out is None:
-        v_out = torch.empty_like(k_out)
+        v_out = _made(stream, torch.empty_like, k_out)
     for t in (k_out, v_out):
         if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype != k_out.dtype:
             raise ValueError(f"k_out, v_out: contiguous {shape} of one type expected, got {t.dtype} {tuple(t.shape)}")
@@ -678,15 +697,15 @@ def milo_kv_select(cache: KvCache, q: torch.Tensor, length: torch.Tensor, n_sel:
     lead = (c.L, c.S, n_q, c.H) if q.dim() == 5 else (c.L, c.S, c.H)
     s = _on(q, stream)
     if selected is None:
-        selected = length.new_empty(lead + (n_sel,))
+        selected = _made(stream, length.new_empty, lead + (n_sel,))
     _int32(selected, lead + (n_sel,), "selected")
     if scores is None and return_scores:
-        scores = q.new_empty(lead + (cache.n_b,), dtype=torch.float32)
+        scores = _made(stream, q.new_empty, lead + (cache.n_b,), dtype=torch.float32)
     if scores is not None and (scores.dtype != torch.float32 or tuple(scores.shape) != lead + (cache.n_b,) or
                                not scores.is_contiguous()):
         raise ValueError(f"scores: contiguous float32 {lead + (cache.n_b,)} expected")
     if workspace is None:
-        workspace = cache.buf.new_empty(cache._ws("milo_kv_select_workspace_size", n_q))
+        workspace = _made(stream, cache.buf.new_empty, cache._ws("milo_kv_select_workspace_size", n_q))
     _same_device(q, length, selected, scores, workspace, cache.buf)
     rc = lib().milo_kv_select(c, cache.buf.data_ptr(), cache.buf.numel(), q.data_ptr(), _dtype_code(q.dtype), n_q, Hq,
                               length.data_ptr(), n_sel, n_first, n_last, selected.data_ptr(),
@@ -713,12 +732,12 @@ def milo_kv_attn(cache: KvCache, q: torch.Tensor, length: torch.Tensor, selected
     if selected is not None:
         _int32(selected, tuple(q.shape[:-2]) + (c.H, n_sel), "selected")
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
         raise ValueError("out: like q expected")
-    lse = q.new_empty(q.shape[:-1], dtype=torch.float32) if return_lse else None
+    lse = _made(stream, q.new_empty, q.shape[:-1], dtype=torch.float32) if return_lse else None
     if workspace is None:
-        workspace = cache.buf.new_empty(cache._ws("milo_kv_attn_workspace_size", n_q, Hq, n_sel))
+        workspace = _made(stream, cache.buf.new_empty, cache._ws("milo_kv_attn_workspace_size", n_q, Hq, n_sel))
     _same_device(q, length, selected, out, workspace, cache.buf)
     rc = lib().milo_kv_attn(c, cache.buf.data_ptr(), cache.buf.numel(), q.data_ptr(), _dtype_code(q.dtype), n_q, Hq,
                             length.data_ptr(), None if selected is None else selected.data_ptr(), n_sel, scale,
@@ -746,12 +765,13 @@ def milo_decode_attn_kv(f: Factors, q: torch.Tensor, selected: torch.Tensor, cac
     if kv_selected is not None:
         _int32(kv_selected, (c.L, c.S, c.H, kv_n_sel), "kv_selected")
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
         raise ValueError("out: like q expected")
     n_sel = selected.shape[-1]
     if workspace is None:
-        workspace = _bytes(lib().milo_decode_kv_workspace_size(f.handle, c.S, Hq, n_sel, c, kv_n_sel), q.device)
+        n = lib().milo_decode_kv_workspace_size(f.handle, c.S, Hq, n_sel, c, kv_n_sel)
+        workspace = _made(stream, _bytes, n, q.device)
     _same_device(q, length, selected, positions, kv_selected, out, workspace, cache.buf)
     rc = lib().milo_decode_attn_kv(f.handle, q.data_ptr(), c.S, Hq, selected.data_ptr(),
                                    None if positions is None else positions.data_ptr(), n_sel, float(rope_base), c,

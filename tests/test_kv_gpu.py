@@ -1015,3 +1015,38 @@ def test_int4_values_past_the_limit_are_stored_as_the_limit(dt):
     got, _ = sections(c)
     np.testing.assert_array_equal(got["k"][:, :, :, :8], q)
     np.testing.assert_array_equal(got["kp"][:, :, :, :8], p)
+
+
+def test_results_on_another_stream_are_not_the_current_streams_memory():
+    """What a call makes for `stream` does not take memory that the current stream let go and may still be using."""
+    w = synth.WORKLOADS["toy"]
+    K, V = (t.cuda() for t in synth.workload_cache(w))
+    f = milo.milo_compress(K, V, w.block_len, milo.default_params(factor_dtype="f32"))
+    c = filled(1, 2, 1, 300, 16, "int8", [300, 40])
+    q, length, zero = rnd(72, 1, 2, 4, 128), i32([300, 40]), i32([0, 0])
+    sel, tail = i32([[0, 3], [5, 1]]), rnd(73, 1, 2, 1, 30, 128)
+    side = torch.cuda.Stream()
+    calls = {
+        "rope": lambda s: milo.milo_rope(q.view(1, 8, 128), i32([5]), milo.rope_params(128), stream=s),
+        "read": lambda s: milo.milo_kv_read(c, zero, 40, stream=s),
+        "select": lambda s: milo.milo_kv_select(c, q, length, 3, return_scores=True, stream=s),
+        "attn": lambda s: milo.milo_kv_attn(c, q, length, return_lse=True, stream=s),
+        "decode": lambda s: milo.milo_decode_attn(f, q, sel, stream=s),
+        "tail": lambda s: milo.milo_decode_attn_tail(f, q, sel, tail, tail, i32([30, 7]), stream=s),
+        "decode_kv": lambda s: milo.milo_decode_attn_kv(f, q, sel, c, length, stream=s),
+    }
+    for name, call in calls.items():
+        want = call(None)
+        torch.cuda.synchronize()
+        one = isinstance(want, torch.Tensor)
+        # memory of these sizes that the current stream has just let go
+        torch.cuda.empty_cache()
+        free = [torch.empty(x.shape, dtype=x.dtype, device="cuda") for x in ([want] if one else want) for _ in range(8)]
+        held = {x.data_ptr() for x in free}
+        del free
+        got = call(side)
+        side.synchronize()
+        for x, y in zip([got] if one else got, [want] if one else want):
+            assert x.data_ptr() not in held, name
+            assert torch.equal(x, y), name
+    ok()
