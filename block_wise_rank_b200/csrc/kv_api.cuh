@@ -108,14 +108,18 @@ KvView kv_view(const milo_kv_shape *s, const void *cache) {
     return v;
 }
 
+// query rows within 31 bits (the product of four counts can pass 64)
+bool kv_rows_fit(const milo_kv_shape *s, int32_t n_q, int32_t heads) {
+    return (double)s->L * s->S * n_q * heads <= INT32_MAX;
+}
+
 // the candidates, queries and heads of a select or attention call
 milo_status kv_query_check(const milo_kv_shape *s, const void *q, milo_dtype q_dtype, int32_t n_q, int32_t Hq,
                            const int32_t *len) {
     if (!q || !len || n_q <= 0 || Hq <= 0 || Hq % s->H || !aligned(q, 16) || !aligned(len, 4))
         return MILO_ERR_INVALID_ARG;
     if (!float_dtype(q_dtype)) return MILO_ERR_UNSUPPORTED;
-    if ((int64_t)s->L * s->S * n_q * Hq > INT32_MAX) return MILO_ERR_UNSUPPORTED;
-    return MILO_OK;
+    return kv_rows_fit(s, n_q, Hq) ? MILO_OK : MILO_ERR_UNSUPPORTED;
 }
 
 // grid size for `ctas` thread blocks in x, 0 if there are too many (2^30, so that four items a block still count in 32 bits)
@@ -268,10 +272,15 @@ milo_status kv_attn_launch(const milo_kv_shape *shape, const void *cache, const 
                                            : kv_attn_type<float>(a, p.nt, p.grid, s), "kv attention launch");
 }
 
-// selection of a call: NULL and 0, or ids and how many (their tokens at most 2^30)
+// tokens of a selection: at most 2^30
+bool kv_tokens_fit(const milo_kv_shape *s, int32_t n_sel) {
+    return (int64_t)n_sel * s->block_len <= (int64_t(1) << 30);
+}
+
+// selection of a call: NULL and 0, or ids and how many
 bool kv_selection_ok(const milo_kv_shape *s, const int32_t *selected, int32_t n_sel) {
     if (!selected) return n_sel == 0;
-    return aligned(selected, 4) && n_sel >= 1 && (int64_t)n_sel * s->block_len <= (int64_t(1) << 30);
+    return aligned(selected, 4) && n_sel >= 1 && kv_tokens_fit(s, n_sel);
 }
 
 }  // namespace
@@ -434,7 +443,7 @@ milo_status milo_kv_read(const milo_kv_shape *shape, const void *cache, size_t c
 }
 
 size_t milo_kv_select_workspace_size(const milo_kv_shape *shape, int32_t n_q) {
-    if (!kv_ok(shape) || shape->d != D || n_q <= 0) return 0;
+    if (!kv_ok(shape) || shape->d != D || n_q <= 0 || !kv_rows_fit(shape, n_q, shape->H)) return 0;
     const int64_t n_b = (shape->cap + shape->block_len - 1) / shape->block_len;
     return align_up(sizeof(float) * (size_t)((int64_t)shape->L * shape->S * shape->H * n_q * n_b));
 }
@@ -488,7 +497,9 @@ milo_status milo_kv_select(const milo_kv_shape *shape, const void *cache, size_t
 }
 
 size_t milo_kv_attn_workspace_size(const milo_kv_shape *shape, int32_t n_q, int32_t Hq, int32_t n_sel) {
-    if (!kv_ok(shape) || shape->d != D || n_q <= 0 || Hq <= 0 || Hq % shape->H || n_sel < 0) return 0;
+    if (!kv_ok(shape) || shape->d != D || n_q <= 0 || Hq <= 0 || Hq % shape->H || n_sel < 0 ||
+        !kv_rows_fit(shape, n_q, Hq) || !kv_tokens_fit(shape, n_sel))
+        return 0;
     return kv_attn_plan(shape, n_q, Hq, n_sel).bytes;
 }
 

@@ -273,3 +273,26 @@ def test_rope_yarn_factor_below_one(L):
         assert milo.milo_rope_freqs(p)[1] == pytest.approx(want, rel=1e-15)
         p.attn_factor = 0.25
         assert milo.milo_rope_freqs(p)[1] == 0.25
+
+
+def test_workspace_sizes_of_refused_calls_are_zero(L):
+    s = milo.kv_shape(**SH)
+    b = ctypes.byref(s)
+    sel, att = L.milo_kv_select_workspace_size, L.milo_kv_attn_workspace_size
+    assert sel(b, 2) > 0 and att(b, 2, 8, 0) > 0 and att(b, 2, 8, 4) > 0
+    most = (2 ** 31 - 1) // (2 * 3 * 4)                          # L S H n_q within 31 bits
+    assert sel(b, most) > 0 and sel(b, most + 1) == 0 and sel(b, 2 ** 31 - 1) == 0
+    assert att(b, most, 4, 0) > 0 and att(b, most + 1, 4, 0) == 0 and att(b, 1 << 28, 8, 0) == 0
+    assert att(b, 2, 2 ** 31 - 4, 0) == 0 and att(b, 2, 8, 2 ** 31 - 1) == 0 and att(b, 2, 8, -1) == 0
+    assert att(b, 2, 8, 2 ** 30 // 32) > 0 and att(b, 2, 8, 2 ** 30 // 32 + 1) == 0
+
+
+def test_counts_whose_product_passes_64_bits_are_refused(L):
+    """2^60 query rows in each of 16 sessions: their number is 0 in 64 bits."""
+    s = milo.kv_shape(1, 16, 1, 64, 16, "int8")
+    b, n, W = ctypes.byref(s), milo.milo_kv_cache_size(milo.kv_shape(1, 16, 1, 64, 16, "int8")), 1 << 62
+    big = 1 << 30
+    assert 16 * big * big == 2 ** 64
+    assert L.milo_kv_select(b, P(), n, P(), 0, big, big, P(), 1, 0, 1, P(), None, P(), W, None) == UNS
+    assert L.milo_kv_attn(b, P(), n, P(), 0, big, big, P(), None, 0, 0.0, P(), None, P(), W, None) == UNS
+    assert L.milo_kv_attn_workspace_size(b, big, big, 0) == 0
