@@ -1050,3 +1050,71 @@ def test_results_on_another_stream_are_not_the_current_streams_memory():
             assert x.data_ptr() not in held, name
             assert torch.equal(x, y), name
     ok()
+
+
+def expect_blocks(got, kn, bl, s, start, n, old=None):
+    """Bounds, codes and scales of session s after rows kn [L][H][n][128] went to `start`: blocks that begin inside the
+    range hold these rows alone, the one that goes on holds what it held (`old`) as well."""
+    for b in range(start // bl, -(-(start + n) // bl)):
+        t0, t1 = max(b * bl, start) - start, min((b + 1) * bl, start + n) - start
+        lo, hi = kn[:, :, t0:t1].min(2), kn[:, :, t0:t1].max(2)
+        if start > b * bl:
+            lo, hi = np.minimum(lo, old["bounds"][:, s, :, b, 0]), np.maximum(hi, old["bounds"][:, s, :, b, 1])
+        lo, hi = R.outward(lo, False), R.outward(hi, True)
+        np.testing.assert_array_equal(got["bounds"][:, s, :, b], np.stack([lo, hi], -2))
+        q, p = R.bound_codes(lo, hi)
+        np.testing.assert_array_equal(got["codes"][:, s, :, b], q)
+        np.testing.assert_array_equal(got["scale"][:, s, :, b], p)
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("n", [2, 5, 37])
+def test_append_goes_on_with_a_block_and_writes_rows_again(dtype, dt, n):
+    """Chunks whose seam lies inside a block, then rows written a second time: the block's bounds widen, never narrow."""
+    L, S, H, cap, bl = 2, 2, 2, 160, 32
+    c = make(L, S, H, cap, bl, dtype)
+    first = rnd(74, L, S, H, 45, 128, dtype=dt, scale=2.0)
+    append(c, first, first, [0, 0], [45, 21])
+    at = [45, 21]
+    for step, scale in ((0, 3.0), (1, 0.1), (2, 5.0)):            # the last two write the same rows again
+        old, _ = sections(c)
+        x, y = rnd(75 + step, L, S, H, n, 128, dtype=dt, scale=scale), rnd(78 + step, L, S, H, n, 128, dtype=dt)
+        append(c, x, y, at)
+        ok()
+        got, _ = sections(c)
+        for s in range(S):
+            rows = slice(at[s], at[s] + n)
+            for name, t in (("k", x), ("v", y)):
+                q, p = R.quantise(f32np(t[:, s]), dtype)
+                np.testing.assert_array_equal(got[name][:, s, :, rows], q)
+                np.testing.assert_array_equal(got[name + "p"][:, s, :, rows], p)
+            expect_blocks(got, f32np(x[:, s]), bl, s, at[s], n, old)
+
+
+@pytest.mark.parametrize("dtype", KINDS)
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_append_with_more_items_than_the_gpu_holds(dtype, dt):
+    """A warp walks many rows of an item where the items fill the GPU twice over."""
+    L, S, H, bl, n, cap = 2, 80, 4, 16, 45, 80
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert ((n - 2 + bl) // bl + 1) * L * S * H * 2 >= 32 * sms
+    c = make(L, S, H, cap, bl, dtype)
+    k, v = rnd(81, L, S, H, n, 128, dtype=dt, scale=3.0), rnd(82, L, S, H, n, 128, dtype=dt)
+    old, _ = sections(c)
+    old["bounds"][:] = 0.0
+    c.buf.zero_()                                                 # blocks that go on hold zeros
+    start, count = [(7 * s) % 36 for s in range(S)], [(11 * s) % 46 for s in range(S)]
+    append(c, k, v, start, count)
+    ok()
+    got, _ = sections(c)
+    kn, vn = f32np(k), f32np(v)
+    for s in range(S):
+        m, rows = count[s], slice(start[s], start[s] + count[s])
+        for name, x in (("k", kn), ("v", vn)):
+            q, p = R.quantise(x[:, s, :, :m], dtype)
+            np.testing.assert_array_equal(got[name][:, s, :, rows], q)
+            np.testing.assert_array_equal(got[name + "p"][:, s, :, rows], p)
+            assert not got[name][:, s, :, :start[s]].any() and not got[name + "p"][:, s, :, start[s] + m:].any()
+        if m:
+            expect_blocks(got, kn[:, s, :, :m], bl, s, start[s], m, old)
