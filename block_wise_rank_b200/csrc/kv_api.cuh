@@ -157,7 +157,11 @@ KvAttnPlan kv_attn_plan(const milo_kv_shape *s, int32_t n_q, int32_t Hq, int32_t
     KvAttnPlan p{};
     const int64_t G = Hq / s->H, rows = n_sel ? G : G * n_q;
     // up to 8 rows: two CTAs an SM, bound by memory; up to 16, and selected blocks, whose lines have few rows: two tiles
-    // of 8 a warp; above, 128 rows share a pass (17 queries of 7 heads over e4m3: 102 us in tiles of 16 rows, 52 us wide)
+    // of 8 a warp; above, 128 rows share a pass.  In tiles of 16 rows and wide, in a graph, codes not in L2 (us): 17 queries
+    // of 7 heads over e4m3 102 and 52; 16 lines of 30000 INT8 tokens, bf16, of 119 rows 177 and 99, 63 rows 101 and 94,
+    // 49 rows 101 and 94, 35 rows 82 and 94, 21 rows 65 and 93 (fp32 235 and 115, 130 and 110, 129 and 110, 104 and 109, 79
+    // and 105); e4m3 at 35 rows 102 and 99, INT4 84 and 80; of 2000 tokens 20 to 29 either way up to 63 rows.  Two tiles (17
+    // to 32 rows) over long lines would take less than the wide pass that they get
     p.nt = rows <= 8 ? 1 : rows <= 16 || n_sel ? 2 : 16;
     const int rpt = 8 * p.nt;
     p.row_tiles = (int)((rows + rpt - 1) / rpt);
@@ -170,9 +174,17 @@ KvAttnPlan kv_attn_plan(const milo_kv_shape *s, int32_t n_q, int32_t Hq, int32_t
     const int64_t lines = (int64_t)p.classes * s->L * s->H, behind = (tiles + warps - 1) / warps;
     const int most = p.nt == 1 ? KaShape<1>::WHOLE : p.nt == 2 ? KaShape<2>::WHOLE : KaShape<16>::WHOLE;
     // short lines, no more than a wave holds: a CTA for each, one launch and nothing to merge; twice as long ones where
-    // they fill a quarter of the wave.  INT8, 7 bf16 heads a KV head, split against whole: 128 lines of 1000 tokens 19.0
-    // and 12.3 us, of 2000 24.6 and 18.5, 256 of 2000 36.6 and 28.8; 4 of 400 11.0 and 8.3, 2 of 1024 10.8 and 12.3;
-    // one of 2048 among 255 of 100 16.4 and 18.5; 256 of 4000 and more as fast or faster split
+    // they fill a quarter of the wave.  The lengths are on the device, so the limits go by capacity, and lie where lines
+    // that fill up take no more time on average (1/6, 1/2 and 5/6 full), whole less split in us, in a graph, codes not in L2:
+    //   up to 8 rows a line (limit 8 units, 1024 tokens), 1, 4 and 16 lines
+    //     capacity 1024: INT8 bf16 7 heads -1.4 -1.6 -2.3, fp32 8 heads -0.6 -1.0 -1.8, e4m3 fp32 4 heads 0.0 -0.2 -0.7
+    //     capacity 1536: -0.5 -0.8 -1.9, +0.5 +0.3 -1.2, +1.9 +2.0 +0.2
+    //     full lines of 1024: 0.0 0.0 -1.0, +2.1 +1.4 0.0, +3.8 +3.4 +2.1; of 512: -1.4 -1.7 -2.1, -1.0 -1.4 -1.4, 0.0 -0.3 -0.3
+    //   up to 16 rows (8 units, 512 tokens), 12 bf16 heads, 1, 4 and 16 lines: 512 -1.8 -3.0 -3.5, 1024 +1.1 +0.1 -5.5
+    //   128 rows (1 unit, 128 tokens), 17 fp32 queries of 7 heads, full: 128 -2.1 to -3.7, 256 +1.7 +1.0 +0.3 (1, 4, 16 lines)
+    // and for a quarter of the wave and more, full lines, whole and split: 74 lines of 2048 18.1 and 22.9, 148 20.5 and
+    // 28.7, 256 30.4 and 36.9, but one of 2048 among lines of 100 tokens 17.1 and 15.7, 17.4 and 16.0, 18.4 and 16.0; 32
+    // lines of 2048 17.4 and 18.8; 74 of 4096 29.4 and 28.7, 200 50.2 and 48.8
     const int wave = ctas * sm_count();
     p.whole = lines <= wave && behind <= (4 * lines >= wave ? 2 * most : most);
     p.grid = (int)(p.whole ? lines : std::min<int64_t>(lines * (begin + behind), wave));
@@ -469,10 +481,13 @@ milo_status milo_kv_select(const milo_kv_shape *shape, const void *cache, size_t
     cudaStream_t s = (cudaStream_t)stream;
     cudaEvent_t t0 = tmark(s);
     cudaError_t e;
-    // a CTA for each row and one launch, where the rows fill most of the SMs, or where they are short and read once (two
-    // launches against one, 7 bf16 heads unless said): 128 rows of 512 blocks 17.0 and 12.3 us, of 1024 19.9 and 15.4, of 2048
-    // 22.3 and 20.2; 80 rows of 1024 14.4 and 16.4; 2 of 512 10.3 to 14.3 (the host's time) and 10.3 to 11.1, with 12 heads,
-    // which take two passes, 12.3 and 14.4
+    // a CTA for each row and one launch, where the rows fill most of the SMs, or where they are short and read once.  One
+    // launch and two, full rows of 7 bf16 heads, in a graph, codes not in L2 (us): 128 rows of 512 blocks 15.0 and 18.1, of 1024
+    // 18.1 and 21.9, of 2048 24.6 and 27.0; 111 rows of 2048 23.6 and 25.3; 80 rows of 1024 16.7 and 16.4, of 2048 22.5
+    // and 20.5.  Short rows are level in a graph and spare a host that makes the calls one by one the second launch
+    // (15.8 and 18.2 for 2 rows of 512): one less two, rows 1/6, 1/2 and 5/6 full on average, 1, 8 and 32 rows of 256 blocks
+    // -0.2 -0.6 -0.8, of 512 +0.6 -0.2 -0.3 (full +1.7 +1.0 +0.3), of 640 +0.9 +0.7 +0.2 (full +2.0 +2.4 +1.4); with 12
+    // heads, which take two passes, full rows of 512 15.0 and 11.6
     const bool fill = 4 * (int64_t)rows >= 3 * sm_count(), brief = a.c.n_b <= 512 && a.G <= KV_SCORE_G;
     if (rows <= (unsigned)sm_count() && a.c.n_b <= KV_ROW_THREADS * KV_ROW_KEYS && (fill || brief)) {
         if (q_dtype == MILO_BF16) k_kv_select_row<__nv_bfloat16><<<rows, KV_ROW_THREADS, 0, s>>>(a);
