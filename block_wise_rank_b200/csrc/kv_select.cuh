@@ -15,6 +15,8 @@
 // A CTA is a chain of latencies: its length, its queries' coding, then steps of one
 // batch of loads (two batches in flight cost registers, 25 us in all; equal runs of steps
 // by the lengths begin more rows, 24 us), and for the selection 6 to 9 us of short rounds.
+// Of the 11.7 cycles between a warp's instructions in the one kernel 3.5 are loads from memory,
+// 1.8 fixed latencies and 1.6 barriers; issue 35 %, DRAM 21 %.
 #pragma once
 #include "kv_cache.cuh"
 

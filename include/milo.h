@@ -470,8 +470,8 @@ size_t milo_kv_cache_size(const milo_kv_shape *shape);   /* 0 on an invalid shap
 milo_status milo_kv_layout(const milo_kv_shape *shape, size_t *offsets);
 
 /*
- * Quantise n_new tokens of every session behind the ones it holds: token i of
- * session s goes to row start[s] + i.
+ * Quantise n_new tokens (0 .. cap) of every session behind the ones it holds:
+ * token i of session s goes to row start[s] + i.
  *   cache:    cache_bytes >= milo_kv_cache_size
  *   k, v:     device, in_dtype (MILO_F32 or MILO_BF16), 16-byte aligned, rows of
  *             128 contiguous values; row (l, s, h, i) starts at element
@@ -495,7 +495,7 @@ milo_status milo_kv_append(const milo_kv_shape *shape, void *cache, size_t cache
                            const int32_t *count, milo_stream_t stream);
 
 /*
- * Read rows start[s] .. start[s] + n - 1 of every session back as values:
+ * Read rows start[s] .. start[s] + n - 1 (n 0 .. cap) of every session back as values:
  * k_out, v_out [L][S][H][n][d] (device, 16-byte aligned, out_dtype MILO_F32 or
  * MILO_BF16; either may be NULL).  start, count and their errors as in
  * milo_kv_append; rows behind count[s] are left as they were.
