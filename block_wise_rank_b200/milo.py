@@ -7,8 +7,8 @@ missing or fails to load, every call raises.
 
 A call with `stream` runs there, and what it makes itself (outputs, workspaces)
 is that stream's memory, as if it were called under torch.cuda.stream(stream): its
-inputs have to be ready on that stream, and another stream that reads its outputs
-waits for it first.
+inputs have to be ready on that stream and stay until it has used them
+(Tensor.record_stream), and another stream that reads its outputs waits for it first.
 """
 from __future__ import annotations
 

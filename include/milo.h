@@ -582,8 +582,8 @@ size_t milo_decode_kv_workspace_size(const milo_factors *f, int32_t S, int32_t H
  * kv_selected [L][S][H][kv_n_sel] of the cache, as milo_kv_attn with n_q = 1 and
  * scale 1 / sqrt(d).  shape's L, S, H and d are the call's.  An empty cache for
  * every session gives milo_decode_attn's output bit for bit.  A query that is not
- * finite, or whose scores in the cache are not, gets NaN in its own row alone where
- * its session sees a cached token.
+ * finite gets NaN, in its own row alone, where it sees a cached token; so does one
+ * with a score in the cache above fp32's largest.
  */
 milo_status milo_decode_attn_kv(const milo_factors *f, const float *q, int32_t S, int32_t Hq, const int32_t *selected,
                                 const int32_t *positions, int32_t n_sel, double rope_base, const milo_kv_shape *shape,
