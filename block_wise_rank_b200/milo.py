@@ -5,10 +5,9 @@ kernels.  Tensors are passed as raw device (or host) pointers; PyTorch is
 used for device memory and streams.  There is no fallback: if libmilo.so is
 missing or fails to load, every call raises.
 
-A call with `stream` runs there, and what it makes itself (outputs, workspaces)
-is that stream's memory, as if it were called under torch.cuda.stream(stream): its
-inputs have to be ready on that stream and stay until it has used them
-(Tensor.record_stream), and another stream that reads its outputs waits for it first.
+A call with `stream` runs as if it were made under torch.cuda.stream(stream): what it
+makes itself (outputs, workspaces) is that stream's memory.  Its inputs have to be
+ready on that stream, and another stream that reads its outputs waits for it first.
 """
 from __future__ import annotations
 
@@ -196,18 +195,28 @@ def _stream(stream=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _made(stream, make, *args, **kw):
-    """make(*args, **kw) in the memory of the stream that a call runs on: taken from the current stream's,
-    `stream` would use it beside earlier work that may still be under way there.  The allocator is told of the
-    current stream too, whose program goes on with the tensor."""
-    if stream is None:
-        return make(*args, **kw)
+def _tensors(x):
+    """The CUDA tensors of a call's arguments or results."""
+    if isinstance(x, torch.Tensor):
+        return [x] if x.is_cuda else []
+    if isinstance(x, (tuple, list)):
+        return [t for y in x for t in _tensors(y)]
+    x = getattr(x, "buf", getattr(x, "arena", None))                # KvCache, Factors
+    return [x] if isinstance(x, torch.Tensor) and x.is_cuda else []
+
+
+def _under(stream, call, *args):
+    """call(*args) on `stream`, in that stream's memory: taken from the current stream's, an output or workspace
+    would be used beside earlier work that may still be under way there.  The allocator is told that the arguments
+    are used on `stream`, and the results by the current stream's program."""
     now = torch.cuda.current_stream(stream.device)
     with torch.cuda.stream(stream):
-        t = make(*args, **kw)
-    if t.is_cuda:
+        r = call(*args)
+    for t in _tensors(args):
+        t.record_stream(stream)
+    for t in _tensors(r):
         t.record_stream(now)
-    return t
+    return r
 
 
 def _dtype_code(t: torch.dtype) -> int:
@@ -299,6 +308,8 @@ def milo_compress(K: torch.Tensor, V: torch.Tensor, block_len: int, params=None,
     """Compress caches K (pre-RoPE) and V, [L][H][T][d] device tensors.  With
     `starts` (n_b + 1 token offsets) the blocks have variable lengths and
     block_len is the longest."""
+    if stream is not None:
+        return _under(stream, milo_compress, K, V, block_len, params, workspace, arena, None, starts)
     assert K.shape == V.shape and K.dtype == V.dtype and K.is_cuda and V.is_cuda
     assert K.is_contiguous() and V.is_contiguous()
     L, H, T, d = K.shape
@@ -309,13 +320,13 @@ def milo_compress(K: torch.Tensor, V: torch.Tensor, block_len: int, params=None,
     if ws_n == 0 or ar_n == 0:
         raise MiloError(MILO_ERR_INVALID_ARG, "milo_compress sizes")
     if workspace is None:
-        workspace = _made(stream, _bytes, ws_n, K.device)
+        workspace = _bytes(ws_n, K.device)
     if arena is None:
-        arena = _made(stream, _bytes, ar_n, K.device)
+        arena = _bytes(ar_n, K.device)
     h = ctypes.c_void_p()
     s = lib().milo_compress(ctypes.byref(shape), _ptr(K), _ptr(V), ctypes.byref(params), _ptr(workspace),
                             workspace.numel() * workspace.element_size(), _ptr(arena),
-                            arena.numel() * arena.element_size(), ctypes.byref(h), _stream(stream))
+                            arena.numel() * arena.element_size(), ctypes.byref(h), _stream())
     _check(s, "milo_compress")
     return Factors(h, arena, shape, params)
 
@@ -327,14 +338,17 @@ def milo_allocate_workspace_size(n_groups: int, n_b: int, d: int = 128) -> int:
 def milo_allocate(sigma: torch.Tensor, eps: torch.Tensor, n_groups: int, n_b: int, T: int, block_len: int,
                   R: int, r_min: int = 0, r_max: int = 0, ranks_out=None, workspace=None, stream=None):
     """Ranks int32 [n_groups * n_b] for sigma float32 [n_groups*n_b][128], eps float64 [n_groups]."""
+    if stream is not None:
+        return _under(stream, milo_allocate, sigma, eps, n_groups, n_b, T, block_len, R, r_min, r_max,
+                      ranks_out, workspace)
     assert sigma.dtype == torch.float32 and eps.dtype == torch.float64 and sigma.is_contiguous()
     d = sigma.shape[-1]
     if ranks_out is None:
-        ranks_out = _made(stream, torch.empty, n_groups * n_b, dtype=torch.int32, device=sigma.device)
+        ranks_out = torch.empty(n_groups * n_b, dtype=torch.int32, device=sigma.device)
     if workspace is None:
-        workspace = _made(stream, _bytes, milo_allocate_workspace_size(n_groups, n_b, d), sigma.device)
+        workspace = _bytes(milo_allocate_workspace_size(n_groups, n_b, d), sigma.device)
     s = lib().milo_allocate(_ptr(sigma), _ptr(eps), n_groups, n_b, d, T, block_len, int(R), r_min, r_max,
-                            _ptr(ranks_out), _ptr(workspace), workspace.numel(), _stream(stream))
+                            _ptr(ranks_out), _ptr(workspace), workspace.numel(), _stream())
     _check(s, "milo_allocate")
     return ranks_out
 
@@ -343,12 +357,15 @@ def milo_allocate_noalloc(sigma: torch.Tensor, eps: torch.Tensor, n_groups: int,
                           R: int, r_min: int = 0, r_max: int = 0, ranks_out=None, stream=None):
     """milo_allocate without a workspace: the library's built-in device scratch
     (at most MILO_NOALLOC_MAX_BLOCKS blocks) stands in for it."""
+    if stream is not None:
+        return _under(stream, milo_allocate_noalloc, sigma, eps, n_groups, n_b, T, block_len, R, r_min, r_max,
+                      ranks_out)
     assert sigma.dtype == torch.float32 and eps.dtype == torch.float64 and sigma.is_contiguous()
     d = sigma.shape[-1]
     if ranks_out is None:
-        ranks_out = _made(stream, torch.empty, n_groups * n_b, dtype=torch.int32, device=sigma.device)
+        ranks_out = torch.empty(n_groups * n_b, dtype=torch.int32, device=sigma.device)
     s = lib().milo_allocate_noalloc(_ptr(sigma), _ptr(eps), n_groups, n_b, d, T, block_len, int(R), r_min, r_max,
-                                    _ptr(ranks_out), _stream(stream))
+                                    _ptr(ranks_out), _stream())
     _check(s, "milo_allocate_noalloc")
     return ranks_out
 
@@ -360,6 +377,8 @@ def milo_decode_workspace_size(f: Factors, S: int, Hq: int, n_sel: int) -> int:
 def milo_decode_attn(f: Factors, q: torch.Tensor, selected: torch.Tensor, positions=None, rope_base=1e6,
                      out=None, workspace=None, stream=None):
     """GQA decode attention over the selected compressed blocks; q [L][S][Hq][d] fp32."""
+    if stream is not None:
+        return _under(stream, milo_decode_attn, f, q, selected, positions, rope_base, out, workspace)
     assert q.dtype == torch.float32 and q.is_contiguous() and q.is_cuda
     L, S, Hq, d = q.shape
     n_sel = selected.shape[1]
@@ -367,11 +386,11 @@ def milo_decode_attn(f: Factors, q: torch.Tensor, selected: torch.Tensor, positi
     if positions is not None:
         assert positions.dtype == torch.int32 and positions.shape == selected.shape and positions.is_contiguous()
     if out is None:
-        out = _made(stream, torch.empty_like, q)
+        out = torch.empty_like(q)
     if workspace is None:
-        workspace = _made(stream, _bytes, milo_decode_workspace_size(f, S, Hq, n_sel), q.device)
+        workspace = _bytes(milo_decode_workspace_size(f, S, Hq, n_sel), q.device)
     s = lib().milo_decode_attn(f.handle, _ptr(q), S, Hq, _ptr(selected), _ptr(positions), n_sel, float(rope_base),
-                               _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream))
+                               _ptr(out), _ptr(workspace), workspace.numel(), _stream())
     _check(s, "milo_decode_attn")
     return out
 
@@ -386,6 +405,9 @@ def milo_decode_attn_tail(f: Factors, q: torch.Tensor, selected: torch.Tensor, k
     """Decode attention over the selected compressed blocks and each session's
     recent uncompressed tokens: k_tail / v_tail [L][S][H][tail_cap][d] (fp32 or
     bf16, keys already rotated), tail_len int32 [S]."""
+    if stream is not None:
+        return _under(stream, milo_decode_attn_tail, f, q, selected, k_tail, v_tail, tail_len, positions,
+                      rope_base, out, workspace)
     assert q.dtype == torch.float32 and q.is_contiguous() and q.is_cuda
     L, S, Hq, d = q.shape
     n_sel = selected.shape[1]
@@ -398,13 +420,13 @@ def milo_decode_attn_tail(f: Factors, q: torch.Tensor, selected: torch.Tensor, k
     assert k_tail.is_contiguous() and v_tail.is_contiguous()
     assert tail_len.dtype == torch.int32 and tail_len.shape == (S,) and tail_len.is_contiguous()
     if out is None:
-        out = _made(stream, torch.empty_like, q)
+        out = torch.empty_like(q)
     if workspace is None:
-        workspace = _made(stream, _bytes, milo_decode_tail_workspace_size(f, S, Hq, n_sel), q.device)
+        workspace = _bytes(milo_decode_tail_workspace_size(f, S, Hq, n_sel), q.device)
     dt = MILO_BF16 if k_tail.dtype == torch.bfloat16 else MILO_F32
     s = lib().milo_decode_attn_tail(f.handle, _ptr(q), S, Hq, _ptr(selected), _ptr(positions), n_sel,
                                     float(rope_base), _ptr(k_tail), _ptr(v_tail), dt, k_tail.shape[3],
-                                    _ptr(tail_len), _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream))
+                                    _ptr(tail_len), _ptr(out), _ptr(workspace), workspace.numel(), _stream())
     _check(s, "milo_decode_attn_tail")
     return out
 
@@ -426,6 +448,8 @@ def milo_decode_attn_offload(f: Factors, q: torch.Tensor, selected: torch.Tensor
                              out=None, workspace=None, stream=None):
     """milo_decode_attn for a handle whose arena is in pinned host memory: the
     selected blocks' factors are staged on the device each call."""
+    if stream is not None:
+        return _under(stream, milo_decode_attn_offload, f, q, selected, positions, rope_base, out, workspace)
     assert q.dtype == torch.float32 and q.is_contiguous() and q.is_cuda
     L, S, Hq, d = q.shape
     n_sel = selected.shape[1]
@@ -433,12 +457,12 @@ def milo_decode_attn_offload(f: Factors, q: torch.Tensor, selected: torch.Tensor
     if positions is not None:
         assert positions.dtype == torch.int32 and positions.shape == selected.shape and positions.is_contiguous()
     if out is None:
-        out = _made(stream, torch.empty_like, q)
+        out = torch.empty_like(q)
     if workspace is None:
-        workspace = _made(stream, _bytes, milo_decode_offload_workspace_size(f, S, Hq, n_sel), q.device)
+        workspace = _bytes(milo_decode_offload_workspace_size(f, S, Hq, n_sel), q.device)
     s = lib().milo_decode_attn_offload(f.handle, _ptr(q), S, Hq, _ptr(selected), _ptr(positions), n_sel,
                                        float(rope_base), _ptr(out), _ptr(workspace), workspace.numel(),
-                                       _stream(stream))
+                                       _stream())
     _check(s, "milo_decode_attn_offload")
     return out
 
@@ -448,17 +472,19 @@ def milo_bm25_select(tables, vocab: int, n_sel: int, k1: float = 1.2, beta: floa
     """BM25 block retrieval on the GPU.  tables = (blk_ptr, blk_term, blk_tf,
     blk_len, q_ptr, q_term, q_tf), int32 (any device).  Returns (selected
     int32 [S][n_sel], scores fp64 [S][n_b]) on `device`."""
-    t = [_made(stream, lambda y: y.to(device=device, dtype=torch.int32).contiguous(), x) for x in tables]
+    if stream is not None:
+        return _under(stream, milo_bm25_select, tables, vocab, n_sel, k1, beta, device, workspace)
+    t = [x.to(device=device, dtype=torch.int32).contiguous() for x in tables]
     blk_ptr, blk_term, blk_tf, blk_len, q_ptr, q_term, q_tf = t
     n_b, S = blk_len.numel(), q_ptr.numel() - 1
-    selected = _made(stream, torch.empty, S, n_sel, dtype=torch.int32, device=device)
-    scores = _made(stream, torch.empty, S, n_b, dtype=torch.float64, device=device)
+    selected = torch.empty(S, n_sel, dtype=torch.int32, device=device)
+    scores = torch.empty(S, n_b, dtype=torch.float64, device=device)
     if workspace is None:
-        workspace = _made(stream, _bytes, lib().milo_bm25_workspace_size(n_b, vocab, S), device)
+        workspace = _bytes(lib().milo_bm25_workspace_size(n_b, vocab, S), device)
     s = lib().milo_bm25_select(_ptr(blk_ptr), _ptr(blk_term), _ptr(blk_tf), _ptr(blk_len), n_b, blk_term.numel(),
                                vocab, _ptr(q_ptr), _ptr(q_term), _ptr(q_tf), S, q_term.numel(), float(k1),
                                float(beta), n_sel, _ptr(selected), _ptr(scores), _ptr(workspace), workspace.numel(),
-                               _stream(stream))
+                               _stream())
     _check(s, "milo_bm25_select")
     return selected, scores
 
@@ -468,6 +494,9 @@ def milo_decode_attn_offload_tail(f: Factors, q: torch.Tensor, selected: torch.T
                                   out=None, workspace=None, stream=None):
     """milo_decode_attn_offload with each session's recent uncompressed tokens
     (device tensors, as milo_decode_attn_tail) in the same softmax."""
+    if stream is not None:
+        return _under(stream, milo_decode_attn_offload_tail, f, q, selected, k_tail, v_tail, tail_len,
+                      positions, rope_base, out, workspace)
     assert q.dtype == torch.float32 and q.is_contiguous() and q.is_cuda
     L, S, Hq, d = q.shape
     n_sel = selected.shape[1]
@@ -476,14 +505,14 @@ def milo_decode_attn_offload_tail(f: Factors, q: torch.Tensor, selected: torch.T
     assert k_tail.shape == v_tail.shape and k_tail.is_contiguous() and v_tail.is_contiguous()
     assert tail_len.dtype == torch.int32 and tail_len.shape == (S,)
     if out is None:
-        out = _made(stream, torch.empty_like, q)
+        out = torch.empty_like(q)
     if workspace is None:
-        workspace = _made(stream, _bytes, milo_decode_offload_workspace_size(f, S, Hq, n_sel), q.device)
+        workspace = _bytes(milo_decode_offload_workspace_size(f, S, Hq, n_sel), q.device)
     dt = MILO_BF16 if k_tail.dtype == torch.bfloat16 else MILO_F32
     s = lib().milo_decode_attn_offload_tail(f.handle, _ptr(q), S, Hq, _ptr(selected), _ptr(positions), n_sel,
                                             float(rope_base), _ptr(k_tail), _ptr(v_tail), dt, k_tail.shape[3],
                                             _ptr(tail_len), _ptr(out), _ptr(workspace), workspace.numel(),
-                                            _stream(stream))
+                                            _stream())
     _check(s, "milo_decode_attn_offload_tail")
     return out
 
@@ -509,22 +538,14 @@ def milo_rope_freqs(params: milo_rope_params):
     return list(w)[:(params.rotary_dim or params.d) // 2], m.value
 
 
-def _on(t: torch.Tensor, stream) -> int:
-    """The raw stream of a call on t, which lives on the current CUDA device."""
+def _on(t: torch.Tensor) -> int:
+    """The raw current stream of a call on t, which lives on the current CUDA device."""
     if not t.is_cuda:
         raise ValueError(f"tensor on {t.device}, a CUDA tensor expected")
     dev = t.get_device()
     if dev != torch._C._cuda_getDevice():
         raise ValueError(f"tensor on {t.device}, and the current device is cuda:{torch.cuda.current_device()}")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _used_on(stream, *tensors):
-    """Tells the allocator that a call's outputs and workspace, the caller's own too, are used on `stream`."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _same_device(first, *tensors):
@@ -545,11 +566,13 @@ def milo_rope(x: torch.Tensor, positions: torch.Tensor, params: milo_rope_params
     turned to positions int32 [n_pos] (token t takes positions[t % n_pos]);
     transpose=True gives the gradient with respect to x of a gradient x.
     out=x turns in place."""
+    if stream is not None:
+        return _under(stream, milo_rope, x, positions, params, out, out_dtype, transpose)
     if x.dim() != 3 or x.shape[2] != params.d or (x.numel() and x.stride(2) != 1):
         raise ValueError(f"x: [n_tokens][n_heads][{params.d}] with contiguous rows expected, got {tuple(x.shape)}")
-    s = _on(x, stream)
+    s = _on(x)
     if out is None:
-        out = _made(stream, torch.empty_like, x, dtype=out_dtype, memory_format=torch.contiguous_format)
+        out = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
     elif out.shape != x.shape or (out.numel() and out.stride(2) != 1):
         raise ValueError(f"out: {tuple(x.shape)} with contiguous rows expected, got {tuple(out.shape)}")
     n_pos = positions.numel()
@@ -559,7 +582,6 @@ def milo_rope(x: torch.Tensor, positions: torch.Tensor, params: milo_rope_params
     xs, ys = x.stride(), out.stride()
     rc = lib().milo_rope(params, x.data_ptr(), _dtype_code(x.dtype), xs[0], xs[1], out.data_ptr(),
                          _dtype_code(out.dtype), ys[0], ys[1], positions.data_ptr(), n_pos, n, h, transpose, s)
-    _used_on(stream, out)
     _check(rc, "milo_rope")
     return out
 
@@ -624,6 +646,8 @@ def milo_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, start: torc
     """Quantise k, v [L][S][H][n][d] (fp32 or bf16; any strides that k and v
     share, d contiguous) into rows start[s] .. of every session; count int32
     [S]: only the first count[s] tokens."""
+    if stream is not None:
+        return _under(stream, milo_kv_append, cache, k, v, start, count)
     c = cache.shape
     if k.shape != v.shape or k.dtype != v.dtype or k.dim() != 5 or \
             tuple(k.shape[:3]) != (c.L, c.S, c.H) or k.shape[4] != c.d:
@@ -631,7 +655,7 @@ def milo_kv_append(cache: KvCache, k: torch.Tensor, v: torch.Tensor, start: torc
     st = _strides(k)
     if k.numel() and (st != _strides(v) or st[4] != 1):
         raise ValueError("k and v: equal strides and contiguous rows expected")
-    s = _on(k, stream)
+    s = _on(k)
     _int32(start, (c.S,), "start")
     if count is not None:
         _int32(count, (c.S,), "count")
@@ -647,16 +671,18 @@ def milo_kv_read(cache: KvCache, start: torch.Tensor, n: int, count=None, k_out=
                  out_dtype=torch.float32, stream=None):
     """(k, v) [L][S][H][n][d]: rows start[s] .. start[s] + n - 1 as values.
     With count, rows behind count[s] are left as they were in k_out / v_out."""
+    if stream is not None:
+        return _under(stream, milo_kv_read, cache, start, n, count, k_out, v_out, out_dtype)
     c = cache.shape
     shape = (c.L, c.S, c.H, n, c.d)
     if k_out is None:
-        k_out = _made(stream, cache.buf.new_empty, shape, dtype=out_dtype)
+        k_out = cache.buf.new_empty(shape, dtype=out_dtype)
     if v_out is None:
-        v_out = _made(stream, torch.empty_like, k_out)
+        v_out = torch.empty_like(k_out)
     for t in (k_out, v_out):
         if tuple(t.shape) != shape or not t.is_contiguous() or t.dtype != k_out.dtype:
             raise ValueError(f"k_out, v_out: contiguous {shape} of one type expected, got {t.dtype} {tuple(t.shape)}")
-    s = _on(k_out, stream)
+    s = _on(k_out)
     _int32(start, (c.S,), "start")
     if count is not None:
         _int32(count, (c.S,), "count")
@@ -664,7 +690,6 @@ def milo_kv_read(cache: KvCache, start: torch.Tensor, n: int, count=None, k_out=
     rc = lib().milo_kv_read(c, cache.buf.data_ptr(), cache.buf.numel(), n, start.data_ptr(),
                             None if count is None else count.data_ptr(), k_out.data_ptr(), v_out.data_ptr(),
                             _dtype_code(k_out.dtype), s)
-    _used_on(stream, k_out, v_out)
     _check(rc, "milo_kv_read")
     return k_out, v_out
 
@@ -692,26 +717,28 @@ def milo_kv_select(cache: KvCache, q: torch.Tensor, length: torch.Tensor, n_sel:
     """Blocks of the cache picked by each query: int32 [L][S](n_q)[H][n_sel] ids,
     ascending, -1 behind the last; with return_scores also the fp32 scores
     [L][S](n_q)[H][n_b] (-inf: not a candidate)."""
+    if stream is not None:
+        return _under(stream, milo_kv_select, cache, q, length, n_sel, n_first, n_last, selected, scores,
+                      return_scores, workspace)
     c = cache.shape
     n_q, Hq = _kv_queries(cache, q, length)
     lead = (c.L, c.S, n_q, c.H) if q.dim() == 5 else (c.L, c.S, c.H)
-    s = _on(q, stream)
+    s = _on(q)
     if selected is None:
-        selected = _made(stream, length.new_empty, lead + (n_sel,))
+        selected = length.new_empty(lead + (n_sel,))
     _int32(selected, lead + (n_sel,), "selected")
     if scores is None and return_scores:
-        scores = _made(stream, q.new_empty, lead + (cache.n_b,), dtype=torch.float32)
+        scores = q.new_empty(lead + (cache.n_b,), dtype=torch.float32)
     if scores is not None and (scores.dtype != torch.float32 or tuple(scores.shape) != lead + (cache.n_b,) or
                                not scores.is_contiguous()):
         raise ValueError(f"scores: contiguous float32 {lead + (cache.n_b,)} expected")
     if workspace is None:
-        workspace = _made(stream, cache.buf.new_empty, cache._ws("milo_kv_select_workspace_size", n_q))
+        workspace = cache.buf.new_empty(cache._ws("milo_kv_select_workspace_size", n_q))
     _same_device(q, length, selected, scores, workspace, cache.buf)
     rc = lib().milo_kv_select(c, cache.buf.data_ptr(), cache.buf.numel(), q.data_ptr(), _dtype_code(q.dtype), n_q, Hq,
                               length.data_ptr(), n_sel, n_first, n_last, selected.data_ptr(),
                               None if scores is None else scores.data_ptr(), workspace.data_ptr(), workspace.numel(),
                               s)
-    _used_on(stream, selected, scores, workspace)
     _check(rc, "milo_kv_select")
     return (selected, scores) if return_scores else selected
 
@@ -725,25 +752,26 @@ def milo_kv_attn(cache: KvCache, q: torch.Tensor, length: torch.Tensor, selected
     """GQA attention of q [L][S](n_q)[Hq][d] (fp32 or bf16) over the cached
     tokens that each query sees, or those of the blocks in `selected`
     [L][S](n_q)[H][n_sel]; with return_lse also the fp32 log-sum-exp."""
+    if stream is not None:
+        return _under(stream, milo_kv_attn, cache, q, length, selected, scale, out, return_lse, workspace)
     c = cache.shape
     n_q, Hq = _kv_queries(cache, q, length)
     n_sel = 0 if selected is None else _kv_listed(selected)
-    s = _on(q, stream)
+    s = _on(q)
     if selected is not None:
         _int32(selected, tuple(q.shape[:-2]) + (c.H, n_sel), "selected")
     if out is None:
-        out = _made(stream, torch.empty_like, q)
+        out = torch.empty_like(q)
     if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
         raise ValueError("out: like q expected")
-    lse = _made(stream, q.new_empty, q.shape[:-1], dtype=torch.float32) if return_lse else None
+    lse = q.new_empty(q.shape[:-1], dtype=torch.float32) if return_lse else None
     if workspace is None:
-        workspace = _made(stream, cache.buf.new_empty, cache._ws("milo_kv_attn_workspace_size", n_q, Hq, n_sel))
+        workspace = cache.buf.new_empty(cache._ws("milo_kv_attn_workspace_size", n_q, Hq, n_sel))
     _same_device(q, length, selected, out, workspace, cache.buf)
     rc = lib().milo_kv_attn(c, cache.buf.data_ptr(), cache.buf.numel(), q.data_ptr(), _dtype_code(q.dtype), n_q, Hq,
                             length.data_ptr(), None if selected is None else selected.data_ptr(), n_sel, scale,
                             out.data_ptr(), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
                             workspace.numel(), s)
-    _used_on(stream, out, lse, workspace)
     _check(rc, "milo_kv_attn")
     return (out, lse) if return_lse else out
 
@@ -753,32 +781,33 @@ def milo_decode_attn_kv(f: Factors, q: torch.Tensor, selected: torch.Tensor, cac
     """milo_decode_attn_tail with the recent tokens in a quantised cache: q
     [L][S][Hq][d] fp32, length int32 [S] tokens held, kv_selected int32
     [L][S][H][kv_n_sel] blocks of the cache (None: all its tokens)."""
+    if stream is not None:
+        return _under(stream, milo_decode_attn_kv, f, q, selected, cache, length, kv_selected, positions,
+                      rope_base, out, workspace)
     c = cache.shape
     if q.dtype != torch.float32 or q.dim() != 4:
         raise ValueError("q: float32 [L][S][Hq][d] expected")
     _, Hq = _kv_queries(cache, q, length)
     kv_n_sel = 0 if kv_selected is None else _kv_listed(kv_selected)
-    s = _on(q, stream)
+    s = _on(q)
     _int32(selected, (c.S, selected.shape[-1]), "selected")
     if positions is not None:
         _int32(positions, selected.shape, "positions")
     if kv_selected is not None:
         _int32(kv_selected, (c.L, c.S, c.H, kv_n_sel), "kv_selected")
     if out is None:
-        out = _made(stream, torch.empty_like, q)
+        out = torch.empty_like(q)
     if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
         raise ValueError("out: like q expected")
     n_sel = selected.shape[-1]
     if workspace is None:
-        n = lib().milo_decode_kv_workspace_size(f.handle, c.S, Hq, n_sel, c, kv_n_sel)
-        workspace = _made(stream, _bytes, n, q.device)
+        workspace = _bytes(lib().milo_decode_kv_workspace_size(f.handle, c.S, Hq, n_sel, c, kv_n_sel), q.device)
     _same_device(q, length, selected, positions, kv_selected, out, workspace, cache.buf)
     rc = lib().milo_decode_attn_kv(f.handle, q.data_ptr(), c.S, Hq, selected.data_ptr(),
                                    None if positions is None else positions.data_ptr(), n_sel, float(rope_base), c,
                                    cache.buf.data_ptr(), cache.buf.numel(), length.data_ptr(),
                                    None if kv_selected is None else kv_selected.data_ptr(), kv_n_sel, out.data_ptr(),
                                    workspace.data_ptr(), workspace.numel(), s)
-    _used_on(stream, out, workspace)
     _check(rc, "milo_decode_attn_kv")
     return out
 

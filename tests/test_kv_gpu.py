@@ -1118,3 +1118,44 @@ def test_append_with_more_items_than_the_gpu_holds(dtype, dt):
             assert not got[name][:, s, :, :start[s]].any() and not got[name + "p"][:, s, :, start[s] + m:].any()
         if m:
             expect_blocks(got, kn[:, s, :, :m], bl, s, start[s], m, old)
+
+
+def test_entry_points_on_another_stream_give_the_same():
+    """Those that the test above leaves out: compression, allocation, offloaded decode, text retrieval, cache writes."""
+    w = synth.WORKLOADS["toy"]
+    K, V = (t.cuda() for t in synth.workload_cache(w))
+    p = milo.default_params(factor_dtype="f32")
+    sigma = torch.sort(rnd(83, 8, 128).abs(), descending=True).values.contiguous()
+    eps = torch.full((1,), 0.5, dtype=torch.float64, device="cuda")
+    q, sel, tail = rnd(84, 1, 2, 4, 128), i32([[0, 3], [5, 1]]), rnd(85, 1, 2, 1, 30, 128)
+    length, start, count = i32([30, 7]), i32([0, 9]), i32([40, 3])
+    host = milo.factors_to_host(milo.milo_compress(K, V, w.block_len, p))
+    tables, kv = synth.bm25_tables(w), rnd(86, 1, 2, 1, 40, 128)
+    caches = {}
+
+    def append(s):
+        milo.milo_kv_append(caches[s], kv, kv, start, count, stream=s)
+        return caches[s].buf
+    calls = {
+        "compress": lambda s: milo.milo_compress(K, V, w.block_len, p, stream=s),
+        "allocate": lambda s: milo.milo_allocate(sigma, eps, 1, 8, 2048, 256, 100, stream=s),
+        "allocate_noalloc": lambda s: milo.milo_allocate_noalloc(sigma, eps, 1, 8, 2048, 256, 100, stream=s),
+        "offload": lambda s: milo.milo_decode_attn_offload(host, q, sel, stream=s),
+        "offload_tail": lambda s: milo.milo_decode_attn_offload_tail(host, q, sel, tail, tail, length, stream=s),
+        "bm25": lambda s: milo.milo_bm25_select(tables, 8192, 3, stream=s),
+        "append": append,
+    }
+    side = torch.cuda.Stream()
+    for s in (None, side):
+        caches[s] = make(1, 2, 1, 64, 16, "int4")
+    torch.cuda.synchronize()                                      # every input is ready on both streams
+    for name, call in calls.items():
+        want = call(None)
+        torch.cuda.synchronize()
+        got = call(side)
+        side.synchronize()
+        if name == "compress":                                    # the arena's gaps are not written: what it decodes to
+            want, got = (milo.milo_decode_attn(x, q, sel) for x in (want, got))
+        for x, y in zip(*((a,) if isinstance(a, torch.Tensor) else a for a in (got, want))):
+            assert torch.equal(x, y), name
+    ok()
