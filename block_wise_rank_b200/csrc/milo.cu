@@ -793,10 +793,10 @@ milo_status decode_impl(const milo_factors *f, const float *q, int32_t S, int32_
         tpush(MILO_TK_TAIL, t0, tmark(s));
         a.tail_o = tail_o;
         a.tail_ml = tail_ml;
-        a.tail_shows = tail.kv != nullptr;
     }
     t0 = tmark(s);
-    k_combine<float><<<(unsigned)rows, D, 0, s>>>(a, a.part_o);
+    if (tail.kv) k_combine<float, true><<<(unsigned)rows, D, 0, s>>>(a, a.part_o);
+    else k_combine<float, false><<<(unsigned)rows, D, 0, s>>>(a, a.part_o);
     tpush(MILO_TK_COMBINE, t0, tmark(s));
     return cuda_check(cudaGetLastError(), "decode launch");
 }
