@@ -38,8 +38,9 @@
 // INT8: 104 us for 558 MB, 82 % of the measured copy rate (the kernel alone 93 us; codes
 // loaded straight into registers, a tile ahead: 122 us; more CTAs than a wave, 2, 3 and 4
 // times as many: 111, 117 and 123 us).  64 INT4 blocks of 64 tokens for 32 sessions, 2
-// layers: 54 us for 169 MB; there the instructions bound it (about 470 a tile of 16
-// tokens, 190 of them widening the codes).  A short line costs a CTA about 4 us beside its
+// layers: 54 us for 169 MB; there about 470 instructions a tile of 16 tokens, 190 of them
+// widening the codes, in dependent chains of 3.7 warps a scheduler take the time (2.57
+// instructions a cycle of 4, DRAM 41 %).  A short line costs a CTA about 4 us beside its
 // tokens.
 #pragma once
 #include <type_traits>
